@@ -1,0 +1,127 @@
+/*
+ * moe_serving.h -- C ABI of the layer's serving operators on MI355X (gfx950):
+ * expert weights in 8 bits with a scale for each block of 128, the grouped
+ * products and the layer on them, and the layer for a few tokens.  Part of
+ * libmoe.so; types, status codes and conventions are moe.h's (device
+ * pointers, work enqueued on `stream`, arguments checked on the host first,
+ * nothing allocated, values read on the device clamped to what they index).
+ *
+ * Inference only: none of these has a backward pass.  Rows, weights, outputs
+ * and workspaces of these calls begin at multiples of 16 bytes (MOE_ERR_ARG
+ * otherwise).
+ *
+ * The 8-bit format.  A code is e4m3 (OCP: sign, 4 bits of exponent with bias
+ * 7, 3 of mantissa; largest 448, no infinities, 0x7F and 0xFF are NaN).  A
+ * value is code * scale, with one float32 scale for each block:
+ *   activations  a row's 128 consecutive columns        [rows, ceil(cols/128)]
+ *   weights      128 x 128 of the stored [N, K] matrix  [ceil(N/128), ceil(K/128)]
+ * The last block of a dimension is as short as the dimension leaves it.
+ * Weights are stored as a linear layer stores them, [N, K] with K (the summed
+ * dimension) contiguous: 8-bit matrix instructions take operands that are
+ * contiguous along K.  (The bf16 and float32 weights of moe.h are [K, N].)
+ *   w_gate_up_q [E, 2I, d] e4m3: gate rows [0, I), up rows [I, 2I)
+ *   w_gate_up_s [E, 2, ceil(I/128), ceil(d/128)] float32: each half in its own
+ *               blocks, so that a block never crosses from gate to up
+ *   w_down_q    [E, d, I] e4m3;  w_down_s [E, ceil(d/128), ceil(I/128)] float32
+ * Scales that moe_quantize_* write are powers of two; the products take any
+ * finite float32 scale (those of published 8-bit checkpoints).
+ */
+#ifndef TRE_MOE_SERVING_H
+#define TRE_MOE_SERVING_H
+
+#include "moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- quantisation -----------------------------------------------------------
+ * Each block's scale is the smallest power of two s >= amax / 448, 2^-126 at
+ * least; its codes are x / s rounded to the nearest e4m3 value (ties to even).
+ * The division is exact and |x / s| <= 448, so nothing saturates and the codes
+ * do not depend on the order of any operation.  A block that holds an infinity
+ * or a NaN gets a NaN scale and NaN codes (0x7F): products of it are NaN.
+ *   x [rows, cols] dt;  q [rows, cols] e4m3, scale [rows, ceil(cols/128)]
+ *   (outputs).  cols a multiple of 64; rows * cols below 2^31.              */
+moe_status moe_quantize_rows(const void* x, moe_dtype dt, int32_t rows, int32_t cols, void* q, float* scale,
+                             void* stream);
+
+/* A layer's expert weights (moe.h's layouts) in the 8-bit format above, once,
+ * e.g. when a model is loaded.
+ *   w_gate_up [E, d, 2I], w_down [E, I, d] dt (inputs, unchanged)           */
+moe_status moe_quantize_weights(const void* w_gate_up, const void* w_down, moe_dtype dt, int32_t E, int32_t d,
+                                int32_t I, void* w_gate_up_q, float* w_gate_up_s, void* w_down_q, float* w_down_s,
+                                void* stream);
+
+/* ---- grouped products in 8 bits -----------------------------------------------
+ * moe_gate_up_swiglu, moe_down_proj and moe_grouped_ffn on 8-bit rows and
+ * weights.  For row r of expert e and output column n:
+ *   sum over blocks b of xs[r, b] * ws[e, n/128, b] *
+ *       (sum over k in block b of xq[r, k] * wq[e, n, k])
+ * in float32, blocks in ascending order.  gate_up quantises
+ * h = silu(gate) * up as moe_quantize_rows does, from float32; down rounds its
+ * sum to bf16 once.  Rows >= expert_offsets[E] of the outputs are untouched.
+ *   x_q [x_rows, d] e4m3, x_s [x_rows, ceil(d/128)];  row_token: NULL (row r
+ *     is x's row r, and x_rows is not read) or [max_rows], row r is x's row
+ *     row_token[r] (as moe_permute writes it; a row outside [0, x_rows) is
+ *     read as zeros)
+ *   h_q [max_rows, I] e4m3, h_s [max_rows, ceil(I/128)];  y_perm [max_rows, d] bf16
+ * Limits as moe.h's; x_rows * d, max_rows * max(d, I) and one expert's 2*d*I
+ * below 2^31.  moe_grouped_ffn_fp8 needs moe_grouped_ffn_fp8_workspace_size()
+ * bytes for h.                                                             */
+moe_status moe_gate_up_swiglu_fp8(const void* x_q, const float* x_s, const int32_t* expert_offsets, int32_t max_rows,
+                                  int32_t E, int32_t d, int32_t I, const void* w_gate_up_q, const float* w_gate_up_s,
+                                  const int32_t* row_token, int32_t x_rows, void* h_q, float* h_s, void* stream);
+moe_status moe_down_proj_fp8(const void* h_q, const float* h_s, const int32_t* expert_offsets, int32_t max_rows,
+                             int32_t E, int32_t d, int32_t I, const void* w_down_q, const float* w_down_s,
+                             void* y_perm, void* stream);
+size_t moe_grouped_ffn_fp8_workspace_size(int32_t max_rows, int32_t I);
+moe_status moe_grouped_ffn_fp8(const void* x_q, const float* x_s, const int32_t* expert_offsets, int32_t max_rows,
+                               int32_t E, int32_t d, int32_t I, const void* w_gate_up_q, const float* w_gate_up_s,
+                               const void* w_down_q, const float* w_down_s, void* y_perm, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The whole layer on 8-bit weights: moe_forward's arguments and outputs with
+ * bf16 x and out, the token rows quantised once before the grouping's gather.
+ *   workspace >= moe_forward_fp8_workspace_size(T, d, E, k, I) bytes        */
+size_t moe_forward_fp8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I);
+moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I,
+                           const void* w_gate_up_q, const float* w_gate_up_s, const void* w_down_q,
+                           const float* w_down_s, int32_t* topk_idx, float* topk_w, int32_t* expert_offsets,
+                           int32_t* row_token, int32_t* pair_row, void* out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* ---- the layer for a few tokens -------------------------------------------------
+ * moe_forward for a decode step, in two kernels: routing, grouping, the row
+ * gather and gate/up + SwiGLU in the first, the down projection and the
+ * combine in the second.  Only the weights of experts that have rows are
+ * read, each once for up to 64 rows.  The selection and the routing weights
+ * are moe_route_topk's bit for bit; the products' sums run in another order
+ * than moe_forward's (float32; h rounded to dt; the experts' outputs are
+ * summed before they are rounded, once).  The order of every sum depends on
+ * the sizes only, so equal calls give equal bits.
+ *   1 <= T <= MOE_FEW_MAX_TOKENS and T * k <= MOE_FEW_MAX_PAIRS, else
+ *   MOE_ERR_UNSUPPORTED (T == 0: nothing to do); otherwise arguments as
+ *   moe_forward, without the grouping's index outputs
+ *   workspace >= moe_forward_few_workspace_size(T, d, E, k, I, dt) bytes;
+ *   calls that may overlap need workspaces of their own
+ * moe_forward_few_fp8 is the same on 8-bit weights, with bf16 x and out: the
+ * activations and h stay in bf16 (the weights' bytes are what a few tokens
+ * cost, and exact activations are free beside them).                       */
+#define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_MAX_PAIRS 1024
+size_t moe_forward_few_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt);
+moe_status moe_forward_few(const void* x, const float* logits, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I,
+                           const void* w_gate_up, const void* w_down, moe_dtype dt, int32_t* topk_idx, float* topk_w,
+                           void* out, void* workspace, size_t workspace_bytes, void* stream);
+size_t moe_forward_few_fp8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I);
+moe_status moe_forward_few_fp8(const void* x, const float* logits, int32_t T, int32_t d, int32_t E, int32_t k,
+                               int32_t I, const void* w_gate_up_q, const float* w_gate_up_s, const void* w_down_q,
+                               const float* w_down_s, int32_t* topk_idx, float* topk_w, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TRE_MOE_SERVING_H */

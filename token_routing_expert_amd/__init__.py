@@ -14,6 +14,11 @@ Functions carry the C entry points' names:
   moe_combine       routing-weighted sum back to token order
   moe_forward       the whole layer
   moe_tile_weights / moe_forward_tiled   the layer on column-tiled weights
+and, from include/moe_serving.h:
+  moe_quantize_rows / moe_quantize_weights   e4m3 codes with a scale for each block of 128
+  moe_gate_up_swiglu_fp8 / moe_down_proj_fp8 / moe_grouped_ffn_fp8   the grouped products on them
+  moe_forward_fp8   the whole layer on 8-bit expert weights
+  moe_forward_few / moe_forward_few_fp8   the whole layer for a few tokens, in two kernels
 """
 from __future__ import annotations
 
@@ -25,6 +30,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmoe.so")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmoe_debug.so")   # the same entry points, device checks compiled in
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "moe.h")
+SERVING_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "moe_serving.h")
 
 MOE_F32 = 0
 MOE_BF16 = 1
@@ -40,9 +46,9 @@ class MoeError(RuntimeError):
         super().__init__(f"{fn}: {STATUS.get(status, status)} ({msg})")
 
 
-def exported_symbols() -> list[str]:
-    """Names of the functions include/moe.h declares."""
-    text = open(HEADER_PATH).read()
+def exported_symbols(header: str | None = None) -> list[str]:
+    """Names of the functions a header declares (include/moe.h, or e.g. SERVING_HEADER_PATH)."""
+    text = open(HEADER_PATH if header is None else header).read()
     return re.findall(r"^(?:moe_status|size_t|const char\*)\s+(moe_\w+)\s*\(", text, flags=re.M)
 
 
@@ -72,6 +78,18 @@ def open_library(path: str):
         "moe_forward_noalloc": ([p, p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, p, p, p], st),
         "moe_tile_weights": ([p, p, i32, i32, i32, st, p, p, p], st),
         "moe_forward_tiled": ([p, p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, p, p, p, sz, p], st),
+        "moe_quantize_rows": ([p, st, i32, i32, p, p, p], st),
+        "moe_quantize_weights": ([p, p, st, i32, i32, i32, p, p, p, p, p], st),
+        "moe_gate_up_swiglu_fp8": ([p, p, p, i32, i32, i32, i32, p, p, p, i32, p, p, p], st),
+        "moe_down_proj_fp8": ([p, p, p, i32, i32, i32, i32, p, p, p, p], st),
+        "moe_grouped_ffn_fp8_workspace_size": ([i32, i32], sz),
+        "moe_grouped_ffn_fp8": ([p, p, p, i32, i32, i32, i32, p, p, p, p, p, p, sz, p], st),
+        "moe_forward_fp8_workspace_size": ([i32, i32, i32, i32, i32], sz),
+        "moe_forward_fp8": ([p, p, i32, i32, i32, i32, i32, p, p, p, p, p, p, p, p, p, p, p, sz, p], st),
+        "moe_forward_few_workspace_size": ([i32, i32, i32, i32, i32, st], sz),
+        "moe_forward_few": ([p, p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, sz, p], st),
+        "moe_forward_few_fp8_workspace_size": ([i32, i32, i32, i32, i32], sz),
+        "moe_forward_few_fp8": ([p, p, i32, i32, i32, i32, i32, p, p, p, p, p, p, p, p, sz, p], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -487,3 +505,279 @@ def moe_backward(x, w_gate_up, w_down, k: int, dout, logits=None, topk_idx=None,
     if dlg is not None:
         res["dlogits"] = dlg
     return res
+
+
+# ---- serving entry points (include/moe_serving.h) -----------------------------------
+#
+# Tensors of one call live on one GPU, which need not be the current one; what
+# a call allocates itself belongs to the stream it runs on.
+
+FEW_MAX_TOKENS = 64
+FEW_MAX_PAIRS = 1024
+
+
+class _Call:
+    """Where one call runs: the device of its first tensor and its stream."""
+
+    def __init__(self, like, stream):
+        torch = _torch()
+        if not like.is_cuda:
+            raise ValueError("tensors passed to the MoE library must live on the GPU")
+        self.device = like.device
+        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        if self.stream.device != self.device:
+            raise ValueError(f"stream of {self.stream.device}, tensors on {self.device}")
+        self.given = stream is not None
+
+    def empty(self, shape, dtype):
+        torch = _torch()
+        if not self.given:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def tensor(self, t, dtype, shape, name):
+        """t's address, after its type, shape, device and layout are checked."""
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors passed to the MoE library must be contiguous")
+        return t.data_ptr()
+
+    def workspace(self, t, nbytes):
+        torch = _torch()
+        if t is None:
+            return self.empty((max(nbytes, 1),), torch.uint8)
+        if t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"workspace: a contiguous tensor on {self.device} is needed")
+        if t.numel() * t.element_size() < nbytes:
+            raise ValueError(f"workspace holds {t.numel() * t.element_size()} bytes, {nbytes} needed")
+        return t
+
+    def run(self, name, fn, *args):
+        """The C call, with the device current (the library launches on the current device)."""
+        torch = _torch()
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*args, self.stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, self.stream.cuda_stream)
+        if status != 0:
+            raise MoeError(name, status)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def moe_quantize_rows(x, q=None, scale=None, stream=None):
+    """x [rows, cols] bf16 or float32 -> (q [rows, cols] float8_e4m3fn, scale [rows, ceil(cols/128)]
+    float32): each block of 128 columns as codes times a power of two."""
+    torch = _torch()
+    lib = load()
+    rows, cols = x.shape
+    c = _Call(x, stream)
+    px = c.tensor(x, x.dtype, (rows, cols), "x")
+    q = c.empty((rows, cols), torch.float8_e4m3fn) if q is None else q
+    scale = c.empty((rows, _blocks(cols)), torch.float32) if scale is None else scale
+    c.run("moe_quantize_rows", lib.moe_quantize_rows, px, _dt(x), rows, cols,
+          c.tensor(q, torch.float8_e4m3fn, (rows, cols), "q"),
+          c.tensor(scale, torch.float32, (rows, _blocks(cols)), "scale"))
+    return q, scale
+
+
+def moe_quantize_weights(w_gate_up, w_down, stream=None):
+    """Expert weights w_gate_up [E, d, 2I], w_down [E, I, d] (bf16 or float32) in the 8-bit format of the
+    serving calls: (w_gate_up_q [E, 2I, d] float8_e4m3fn, w_gate_up_s [E, 2, ceil(I/128), ceil(d/128)] float32,
+    w_down_q [E, d, I], w_down_s [E, ceil(d/128), ceil(I/128)])."""
+    torch = _torch()
+    lib = load()
+    E, d, two_i = w_gate_up.shape
+    I = two_i // 2
+    if two_i != 2 * I:
+        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)}: the last dimension is 2I")
+    c = _Call(w_gate_up, stream)
+    pgu = c.tensor(w_gate_up, w_gate_up.dtype, (E, d, 2 * I), "w_gate_up")
+    pd = c.tensor(w_down, w_gate_up.dtype, (E, I, d), "w_down")
+    gq = c.empty((E, 2 * I, d), torch.float8_e4m3fn)
+    gs = c.empty((E, 2, _blocks(I), _blocks(d)), torch.float32)
+    dq = c.empty((E, d, I), torch.float8_e4m3fn)
+    ds = c.empty((E, _blocks(d), _blocks(I)), torch.float32)
+    c.run("moe_quantize_weights", lib.moe_quantize_weights, pgu, pd, _dt(w_gate_up), E, d, I, gq.data_ptr(),
+          gs.data_ptr(), dq.data_ptr(), ds.data_ptr())
+    return gq, gs, dq, ds
+
+
+def _weights8(c, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, d):
+    """(E, I, addresses of the four 8-bit weight tensors)."""
+    torch = _torch()
+    E, two_i, d2 = w_gate_up_q.shape
+    I = two_i // 2
+    if d2 != d or two_i != 2 * I:
+        raise ValueError(f"w_gate_up_q {tuple(w_gate_up_q.shape)} does not match d={d}")
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    return E, I, (c.tensor(w_gate_up_q, f8, (E, 2 * I, d), "w_gate_up_q"),
+                  c.tensor(w_gate_up_s, f32, (E, 2, _blocks(I), _blocks(d)), "w_gate_up_s"),
+                  c.tensor(w_down_q, f8, (E, d, I), "w_down_q"),
+                  c.tensor(w_down_s, f32, (E, _blocks(d), _blocks(I)), "w_down_s"))
+
+
+def _routing(c, logits, topk_idx, topk_w, T, E, k):
+    """(address of the logits or None, topk_idx, topk_w, their addresses)."""
+    torch = _torch()
+    plg = None
+    if logits is not None:
+        plg = c.tensor(logits, torch.float32, (T, E), "logits")
+        topk_idx = c.empty((T, k), torch.int32) if topk_idx is None else topk_idx
+        topk_w = c.empty((T, k), torch.float32) if topk_w is None else topk_w
+    elif topk_idx is None or topk_w is None:
+        raise ValueError("without logits, topk_idx and topk_w must be given")
+    return (plg, topk_idx, topk_w, c.tensor(topk_idx, torch.int32, (T, k), "topk_idx"),
+            c.tensor(topk_w, torch.float32, (T, k), "topk_w"))
+
+
+def moe_gate_up_swiglu_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, h_q=None, h_s=None, row_token=None,
+                           max_rows=None, stream=None):
+    """moe_gate_up_swiglu on 8-bit rows (x_q, x_s from moe_quantize_rows) and weights -> (h_q [R, I], h_s
+    [R, ceil(I/128)]).  With ``row_token`` [R], row r is x's row row_token[r]; R = ``max_rows`` (default
+    len(row_token))."""
+    torch = _torch()
+    lib = load()
+    x_rows, d = x_q.shape
+    c = _Call(x_q, stream)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    px, ps = c.tensor(x_q, f8, (x_rows, d), "x_q"), c.tensor(x_s, f32, (x_rows, _blocks(d)), "x_s")
+    R, pt = x_rows, None
+    if row_token is not None:
+        R = int(max_rows if max_rows is not None else row_token.shape[0])
+        pt = c.tensor(row_token, torch.int32, (row_token.shape[0],), "row_token")
+        if row_token.shape[0] < R:
+            raise ValueError("row_token holds fewer rows than max_rows")
+    E, two_i, d2 = w_gate_up_q.shape
+    I = two_i // 2
+    pw = c.tensor(w_gate_up_q, f8, (E, 2 * I, d), "w_gate_up_q")
+    pws = c.tensor(w_gate_up_s, f32, (E, 2, _blocks(I), _blocks(d)), "w_gate_up_s")
+    po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    h_q = c.empty((R, I), f8) if h_q is None else h_q
+    h_s = c.empty((R, _blocks(I)), f32) if h_s is None else h_s
+    c.run("moe_gate_up_swiglu_fp8", lib.moe_gate_up_swiglu_fp8, px, ps, po, R, E, d, I, pw, pws, pt, x_rows,
+          c.tensor(h_q, f8, (R, I), "h_q"), c.tensor(h_s, f32, (R, _blocks(I)), "h_s"))
+    return h_q, h_s
+
+
+def moe_down_proj_fp8(h_q, h_s, expert_offsets, w_down_q, w_down_s, y_perm=None, stream=None):
+    """moe_down_proj on 8-bit rows and weights: the grouped product y_perm[r] = h[r] @ Wd[e]^T of the stored
+    [N, K] weights, with a scale for each block of 128 -> y_perm [R, d] bf16."""
+    torch = _torch()
+    lib = load()
+    R, I = h_q.shape
+    E, d, I2 = w_down_q.shape
+    c = _Call(h_q, stream)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    ph, ps = c.tensor(h_q, f8, (R, I), "h_q"), c.tensor(h_s, f32, (R, _blocks(I)), "h_s")
+    pw, pws = (c.tensor(w_down_q, f8, (E, d, I), "w_down_q"),
+               c.tensor(w_down_s, f32, (E, _blocks(d), _blocks(I)), "w_down_s"))
+    po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    y_perm = c.empty((R, d), torch.bfloat16) if y_perm is None else y_perm
+    c.run("moe_down_proj_fp8", lib.moe_down_proj_fp8, ph, ps, po, R, E, d, I, pw, pws,
+          c.tensor(y_perm, torch.bfloat16, (R, d), "y_perm"))
+    return y_perm
+
+
+def moe_grouped_ffn_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, y_perm=None,
+                        workspace=None, stream=None):
+    """moe_grouped_ffn on 8-bit rows grouped by expert_offsets [E+1] and 8-bit weights -> y_perm [R, d] bf16;
+    h is quantised as moe_quantize_rows does."""
+    torch = _torch()
+    lib = load()
+    R, d = x_q.shape
+    c = _Call(x_q, stream)
+    px = c.tensor(x_q, torch.float8_e4m3fn, (R, d), "x_q")
+    ps = c.tensor(x_s, torch.float32, (R, _blocks(d)), "x_s")
+    E, I, pws = _weights8(c, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, d)
+    po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    y_perm = c.empty((R, d), torch.bfloat16) if y_perm is None else y_perm
+    nbytes = lib.moe_grouped_ffn_fp8_workspace_size(R, I)
+    ws = c.workspace(workspace, nbytes)
+    c.run("moe_grouped_ffn_fp8", lib.moe_grouped_ffn_fp8, px, ps, po, R, E, d, I, *pws,
+          c.tensor(y_perm, torch.bfloat16, (R, d), "y_perm"), ws.data_ptr(), nbytes)
+    return y_perm
+
+
+def moe_forward_fp8_workspace_size(T: int, d: int, E: int, k: int, I: int) -> int:
+    return int(load().moe_forward_fp8_workspace_size(T, d, E, k, I))
+
+
+def moe_forward_fp8(x, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, k: int, logits=None, topk_idx=None, topk_w=None,
+                    out=None, expert_offsets=None, row_token=None, pair_row=None, workspace=None, stream=None):
+    """moe_forward on 8-bit expert weights (moe_quantize_weights' four tensors), x and out bf16: the token rows
+    and h are quantised on the way.  Returns (out [T, d], topk_idx, topk_w)."""
+    torch = _torch()
+    lib = load()
+    T, d = x.shape
+    c = _Call(x, stream)
+    px = c.tensor(x, torch.bfloat16, (T, d), "x")
+    E, I, pws = _weights8(c, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, d)
+    plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
+    out = c.empty((T, d), torch.bfloat16) if out is None else out
+    ix = [None if t is None else c.tensor(t, torch.int32, (n,), name)
+          for name, t, n in (("expert_offsets", expert_offsets, E + 1), ("row_token", row_token, T * k),
+                             ("pair_row", pair_row, T * k))]
+    nbytes = lib.moe_forward_fp8_workspace_size(T, d, E, k, I)
+    ws = c.workspace(workspace, nbytes)
+    c.run("moe_forward_fp8", lib.moe_forward_fp8, px, plg, T, d, E, k, I, *pws, pi, pw, *ix,
+          c.tensor(out, torch.bfloat16, (T, d), "out"), ws.data_ptr(), nbytes)
+    return out, topk_idx, topk_w
+
+
+def moe_forward_few_workspace_size(T: int, d: int, E: int, k: int, I: int, dtype) -> int:
+    return int(load().moe_forward_few_workspace_size(T, d, E, k, I, dtype))
+
+
+def moe_forward_few(x, w_gate_up, w_down, k: int, logits=None, topk_idx=None, topk_w=None, out=None, workspace=None,
+                    stream=None):
+    """moe_forward for a few tokens (x [T, d], T <= FEW_MAX_TOKENS, T * k <= FEW_MAX_PAIRS) in two kernels;
+    same weights, routing and arguments.  Returns (out [T, d], topk_idx, topk_w)."""
+    lib = load()
+    T, d = x.shape
+    E, d2, two_i = w_gate_up.shape
+    I = two_i // 2
+    if d2 != d or two_i != 2 * I:
+        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} does not match d={d}")
+    dt = _dt(x)
+    c = _Call(x, stream)
+    px = c.tensor(x, x.dtype, (T, d), "x")
+    pgu = c.tensor(w_gate_up, x.dtype, (E, d, 2 * I), "w_gate_up")
+    pd = c.tensor(w_down, x.dtype, (E, I, d), "w_down")
+    plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
+    out = c.empty((T, d), x.dtype) if out is None else out
+    nbytes = lib.moe_forward_few_workspace_size(T, d, E, k, I, dt)
+    ws = c.workspace(workspace, nbytes)
+    c.run("moe_forward_few", lib.moe_forward_few, px, plg, T, d, E, k, I, pgu, pd, dt, pi, pw,
+          c.tensor(out, x.dtype, (T, d), "out"), ws.data_ptr(), nbytes)
+    return out, topk_idx, topk_w
+
+
+def moe_forward_few_fp8_workspace_size(T: int, d: int, E: int, k: int, I: int) -> int:
+    return int(load().moe_forward_few_fp8_workspace_size(T, d, E, k, I))
+
+
+def moe_forward_few_fp8(x, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, k: int, logits=None, topk_idx=None,
+                        topk_w=None, out=None, workspace=None, stream=None):
+    """moe_forward_few on 8-bit expert weights (moe_quantize_weights' four tensors) with bf16 activations.
+    Returns (out [T, d], topk_idx, topk_w)."""
+    torch = _torch()
+    lib = load()
+    T, d = x.shape
+    c = _Call(x, stream)
+    px = c.tensor(x, torch.bfloat16, (T, d), "x")
+    E, I, pws = _weights8(c, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, d)
+    plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
+    out = c.empty((T, d), torch.bfloat16) if out is None else out
+    nbytes = lib.moe_forward_few_fp8_workspace_size(T, d, E, k, I)
+    ws = c.workspace(workspace, nbytes)
+    c.run("moe_forward_few_fp8", lib.moe_forward_few_fp8, px, plg, T, d, E, k, I, *pws, pi, pw,
+          c.tensor(out, torch.bfloat16, (T, d), "out"), ws.data_ptr(), nbytes)
+    return out, topk_idx, topk_w

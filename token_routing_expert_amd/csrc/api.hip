@@ -1,8 +1,7 @@
 // api.hip -- the C ABI (include/moe.h): host-side validation, workspace
 // carving and kernel launches.  Every argument is checked before anything
 // is enqueued; no call allocates, frees or synchronises.
-#include "../../include/moe.h"
-#include "common.hpp"
+#include "checks.hpp"
 
 #include <mutex>
 
@@ -10,32 +9,7 @@ using namespace tre;
 
 namespace {
 
-constexpr int64_t kMaxElems = (int64_t)1 << 31;  // per-array element limit
 constexpr int32_t kMaxRouterWidth = 1 << 22;       // router projection: d below this
-
-size_t elem_size(moe_dtype dt) { return dt == MOE_F32 ? 4 : 2; }
-bool dtype_ok(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-moe_status check_experts(int32_t E) {
-  if (E < 1) return MOE_ERR_ARG;
-  if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-moe_status check_width(int32_t n) {
-  if (n < 1) return MOE_ERR_ARG;
-  if (n % 64 != 0) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-#define TRY(expr)                    \
-  do {                               \
-    const moe_status st_ = (expr);   \
-    if (st_ != MOE_OK) return st_;   \
-  } while (0)
 
 // Byte layout of the moe_forward workspace.
 struct ForwardLayout {

@@ -58,6 +58,12 @@ __device__ __forceinline__ T clampi(T v, T lo, T hi) {
   return v < lo ? lo : (v > hi ? hi : v);
 }
 
+// A compile-time number as an argument (of a generic lambda).
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
+
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ constexpr int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
@@ -302,5 +308,52 @@ hipError_t launch_gate_up_dgrad_f32(const float* dgu, const int32_t* expert_offs
                                     int d, int I, const float* w_gate_up, float* dx_perm, hipStream_t s);
 hipError_t launch_wgrad_f32(const float* a, int lda, int M, const float* b, int ldb, int N,
                             const int32_t* expert_offsets, int64_t max_rows, int E, float* dw, hipStream_t s);
+
+// ---- 8-bit codes and scales (quantize.hip) ----
+// rows and expert weights to e4m3 with a float32 scale for each block of 128
+// (layouts in include/moe_serving.h)
+hipError_t launch_quantize_rows_bf16(const bf16_t* x, int64_t rows, int cols, uint8_t* q, float* scale,
+                                     hipStream_t s);
+hipError_t launch_quantize_rows_f32(const float* x, int64_t rows, int cols, uint8_t* q, float* scale, hipStream_t s);
+hipError_t launch_quantize_weights_bf16(const bf16_t* wgu, const bf16_t* wd, int E, int d, int I, uint8_t* gu_q,
+                                        float* gu_s, uint8_t* dn_q, float* dn_s, hipStream_t s);
+hipError_t launch_quantize_weights_f32(const float* wgu, const float* wd, int E, int d, int I, uint8_t* gu_q,
+                                       float* gu_s, uint8_t* dn_q, float* dn_s, hipStream_t s);
+
+// ---- grouped products in 8 bits (fp8_ffn.hip) ----
+// xq [x_rows or max_rows, d], wq [E, 2I, d] -> codes hq [max_rows, I] and
+// their scales; with row_token, row r is x's row row_token[r]
+hipError_t launch_gate_up_fp8(const uint8_t* xq, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
+                              int d, int I, const uint8_t* wq, const float* ws, const int32_t* row_token,
+                              int64_t x_rows, uint8_t* hq, float* hs, hipStream_t s);
+// hq [max_rows, I], wq [E, d, I] -> y [max_rows, d]
+hipError_t launch_down_fp8(const uint8_t* hq, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
+                           int d, int I, const uint8_t* wq, const float* ws, bf16_t* y, hipStream_t s);
+
+// ---- the layer for a few tokens (few.hip) ----
+constexpr int kFewTokens = 64;
+constexpr int kFewPairs = 1024;
+constexpr int kFewSplitMax = 8;
+// h [P, I] of the activations' type, part [split, P, d] float32, counters
+// [few_counters(d)]; split from the few_split_* of the weights' type
+struct FewScratch {
+  void* h;
+  float* part;
+  int32_t* counters;
+};
+int few_split_bf16(int P, int E, int d, int I);
+int few_split_f32(int P, int E, int d, int I);
+int few_split_fp8(int P, int E, int d, int I);
+int few_counters(int d);
+// logits null: topk_idx / topk_w are the given pairs
+hipError_t launch_few_bf16(const bf16_t* x, const float* logits, int T, int d, int E, int k, int I, const bf16_t* wgu,
+                           const bf16_t* wd, int32_t* topk_idx, float* topk_w, bf16_t* out, const FewScratch& ws,
+                           hipStream_t s);
+hipError_t launch_few_f32(const float* x, const float* logits, int T, int d, int E, int k, int I, const float* wgu,
+                          const float* wd, int32_t* topk_idx, float* topk_w, float* out, const FewScratch& ws,
+                          hipStream_t s);
+hipError_t launch_few_fp8(const bf16_t* x, const float* logits, int T, int d, int E, int k, int I, const uint8_t* wgu,
+                          const float* wgu_s, const uint8_t* wd, const float* wd_s, int32_t* topk_idx, float* topk_w,
+                          bf16_t* out, const FewScratch& ws, hipStream_t s);
 
 }  // namespace tre

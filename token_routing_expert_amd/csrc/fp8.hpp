@@ -1,0 +1,39 @@
+// fp8.hpp -- the arithmetic of an e4m3 block with its scale, shared by the
+// quantisation kernels and the 8-bit products.
+//
+// A block with largest magnitude amax gets s = 2^n, the smallest power of two
+// with amax <= 448 s (n >= -126), and codes rne_e4m3(x / s).  With amax = m 2^e,
+// m in [1, 2), and 448 = 1.75 * 2^8: n = e - 8 + (m > 1.75), read off amax's bits.
+// Multiplying by 2^-n is exact (a result below 2^-126 rounds to the code 0
+// either way), so the codes are those of the exact quotient and do not depend
+// on the hardware's division; a scale amax / 448 would give quotients that round
+// twice, and gains at most one of e4m3's 18 binades.  Magnitudes are compared
+// as integers (bits without the sign), where infinity and NaN are the largest:
+// a block that holds one shows it in amax, and all its codes become NaN.
+#pragma once
+
+#include "common.hpp"
+
+namespace tre {
+
+constexpr int kBlock = 128;                   // elements a scale covers in a row
+constexpr uint32_t kNan8 = 0x7F7F7F7Fu;       // four NaN codes
+
+// Bits of the scale 2^n for a block whose largest magnitude has these bits,
+// and of 2^-n.
+__device__ __forceinline__ void power_scale(uint32_t amax, float& scale, float& inv, bool& finite) {
+  finite = amax < 0x7F800000u;
+  int n = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  n = n < -126 ? -126 : n;
+  scale = __builtin_bit_cast(float, finite ? (uint32_t)(n + 127) << 23 : 0x7FC00000u);
+  inv = __builtin_bit_cast(float, (uint32_t)(127 - (finite ? n : 0)) << 23);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
+}  // namespace tre
