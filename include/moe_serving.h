@@ -95,7 +95,7 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
  * moe_forward for a decode step, in two kernels: routing, grouping, the row
  * gather and gate/up + SwiGLU in the first, the down projection and the
  * combine in the second.  Only the weights of experts that have rows are
- * read, each once for up to 64 rows.  The selection and the routing weights
+ * read, once for every 64 rows of one (8-bit: 32).  The selection and the routing weights
  * are moe_route_topk's bit for bit; the products' sums run in another order
  * than moe_forward's (float32; h rounded to dt; the experts' outputs are
  * summed before they are rounded, once).  The order of every sum depends on

@@ -37,6 +37,7 @@ template <typename Elem>
 struct RowMajor {
   using Act = Elem;
   static constexpr int V = 16 / (int)sizeof(Elem), NF = V, kStep = 4 * V, kBytes = 16 * V;
+  static constexpr int kGuWaves = 8, kDnWaves = 4, kMaxTiles = 4;
   static constexpr int kXVec = 1;                     // 16-byte activation loads a row and step
   static constexpr int kCols = 16 * V;                // columns of a tile; gate/up: half gate, half up
   struct Args {
@@ -112,7 +113,8 @@ struct RowMajor {
 // a row may be a NaN).
 struct Blocked8 {
   using Act = bf16_t;
-  static constexpr int NF = 2, kStep = 128, kBytes = 32 * NF;
+  static constexpr int NF = 4, kStep = 128, kBytes = 32 * NF;
+  static constexpr int kGuWaves = 4, kDnWaves = 4, kMaxTiles = 2;
   static constexpr int kXVec = 4;
   static constexpr int kCols = 16 * NF;
   struct Args {
@@ -132,9 +134,10 @@ struct Blocked8 {
     Blocked8 m;
     const int ib = (I + 127) / 128, db = (d + 127) / 128;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {   // fragment 0 gate, 1 up
-      m.base[f] = a.w + ((int64_t)e * 2 + f) * I * d + (int64_t)n0 * d;
-      m.scale[f] = a.s + (((int64_t)e * 2 + f) * ib + n0 / 128) * db;
+    for (int f = 0; f < NF; ++f) {   // the lower half of the fragments gate, the upper up
+      const int half = f / (NF / 2), n = n0 + f % (NF / 2) * 16;
+      m.base[f] = a.w + ((int64_t)e * 2 + half) * I * d + (int64_t)n * d;
+      m.scale[f] = a.s + (((int64_t)e * 2 + half) * ib + n / 128) * db;
     }
     m.set(d, lane);
     return m;
@@ -199,7 +202,7 @@ struct Blocked8 {
     }
   }
   __device__ __forceinline__ static int gate_slot(int c) { return c; }
-  __device__ __forceinline__ static int up_slot(int c) { return 16 + c; }
+  __device__ __forceinline__ static int up_slot(int c) { return NF / 2 * 16 + c; }
   __device__ __forceinline__ static int down_slot(int c) { return c; }
 };
 
@@ -213,18 +216,18 @@ __device__ __forceinline__ void few_store4(bf16_t* p, f32x4 f) {
 }
 __device__ __forceinline__ void few_store4(float* p, f32x4 f) { *(f32x4*)p = f; }
 
-// A workgroup's share of the grouping, from the pairs' expert ids in LDS.
+// The grouping, in every workgroup, from the pairs' expert ids in LDS.
 struct FewGroup {
-  int32_t idx[kFewPairs];    // expert of each pair
-  int32_t list[kFewPairs];   // this workgroup's expert's pairs, ascending
+  int32_t idx[kFewPairs];      // expert of each pair
+  int32_t list[kFewPairs];     // one expert's pairs, ascending
   int32_t count[kMaxExperts];
-  int32_t e, n, n_live;      // expert of the slot, its pairs, experts with pairs
+  int32_t live[kMaxExperts];   // the experts that have pairs, ascending
+  int32_t n_live;
 };
 
-// The slot-th expert that has pairs (n_live of them), and its pairs.  False
-// when there are fewer.  An id outside [0, E) belongs to no expert.
+// Counts and live experts.  An id outside [0, E) belongs to no expert.
 template <int NT>
-__device__ __forceinline__ bool few_group(FewGroup& g, int P, int E, int slot) {
+__device__ __forceinline__ void few_group(FewGroup& g, int P, int E) {
   const int tid = threadIdx.x, lane = tid % kWave;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (kWave - lane);
   for (int e = tid; e < kMaxExperts; e += NT) g.count[e] = 0;
@@ -236,19 +239,24 @@ __device__ __forceinline__ bool few_group(FewGroup& g, int P, int E, int slot) {
   }
   __syncthreads();
   if (tid < kWave) {
-    int before = 0;
+    int n = 0;
     for (int b = 0; b < E; b += kWave) {
       const bool has = g.count[b + lane] > 0;   // zero past E (E <= 256 = four waves of counts)
       const uint64_t m = __ballot(has);
-      if (has && before + __popcll(m & below) == slot) g.e = b + lane;
-      before += __popcll(m);
+      if (has) g.live[n + __popcll(m & below)] = b + lane;
+      n += __popcll(m);
     }
-    if (lane == 0) g.n_live = before;
+    if (lane == 0) g.n_live = n;
   }
   __syncthreads();
-  if (slot >= g.n_live) return false;
-  if (tid < kWave) {
-    const int e = g.e;
+}
+
+// The pairs of expert e, into g.list (read by everyone after this).
+__device__ __forceinline__ void few_list(FewGroup& g, int P, int e) {
+  const int lane = threadIdx.x % kWave;
+  const uint64_t below = lane == 0 ? 0ull : ~0ull >> (kWave - lane);
+  __syncthreads();   // the last list's readers are done
+  if (threadIdx.x < kWave) {
     int n = 0;
     for (int b = 0; b < P; b += kWave) {
       const bool hit = b + lane < P && g.idx[b + lane] == e;
@@ -256,10 +264,8 @@ __device__ __forceinline__ bool few_group(FewGroup& g, int P, int E, int slot) {
       if (hit) g.list[n + __popcll(m & below)] = b + lane;
       n += __popcll(m);
     }
-    if (lane == 0) g.n = n;
   }
   __syncthreads();
-  return true;
 }
 
 // Every token's selection, into LDS: the lane groups of the routing kernel
@@ -369,23 +375,23 @@ __device__ __forceinline__ float few_sum(const float* red, int row, int slot) {
 }
 
 // ---- gate/up -----------------------------------------------------------------
-// grid (column tiles of kCols / 2 columns of h, slots).  Workgroup (0, 0) also
-// writes the selection and clears the column tiles' counters for k_few_down.
-constexpr int kGuWaves = 8;
-
+// Items (live expert, column tile of kCols / 2 columns of h), dealt round-robin
+// to the workgroups, so that routing and grouping are done once a workgroup.
+// The first one also writes the selection and clears the column tiles'
+// counters for k_few_down.
 template <class M, int MT>
-__global__ __launch_bounds__(kGuWaves * kWave) void k_few_gate_up(
+__global__ __launch_bounds__(M::kGuWaves * kWave) void k_few_gate_up(
     const typename M::Act* __restrict__ x, const float* __restrict__ logits, int32_t* __restrict__ topk_idx,
     float* __restrict__ topk_w, int T, int d, int E, int k, int I, typename M::Args wa,
     typename M::Act* __restrict__ h, int32_t* __restrict__ counters, int n_counters) {
-  constexpr int NW = kGuWaves, NT = NW * kWave, CT = M::kCols / 2;
+  constexpr int NW = M::kGuWaves, NT = NW * kWave, CT = M::kCols / 2;
   __shared__ FewGroup g;
   __shared__ float red[NW * 16 * kRedStride<M>];
   float* s_w = red;   // routing weights, before the sums need the buffer
   static_assert(kFewPairs <= NW * 16 * kRedStride<M>, "routing weights fit the reduction buffer");
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int P = T * k, n0 = blockIdx.x * CT;
-  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+  const int P = T * k;
+  const bool first = blockIdx.x == 0;
   if (logits) {
     few_route<NT>(logits, T, E, k, g.idx, s_w);
     if (first) {
@@ -400,114 +406,142 @@ __global__ __launch_bounds__(kGuWaves * kWave) void k_few_gate_up(
   }
   if (first)
     for (int c = tid; c < n_counters; c += NT) counters[c] = 0;
-  if (!few_group<NT>(g, P, E, blockIdx.y)) return;
+  few_group<NT>(g, P, E);
 
-  const M w = M::gate_up(wa, __builtin_amdgcn_readfirstlane(g.e), d, I, n0, lane);
-  const int n = __builtin_amdgcn_readfirstlane(g.n), steps = (d + M::kStep - 1) / M::kStep;
-  few_row_tiles<MT>(n, [&](auto count, int r0) {
-    constexpr int C = decltype(count)::value;
-    const typename M::Act* xr[C];
-#pragma unroll
-    for (int m = 0; m < C; ++m) {
-      const int r = r0 + m * 16 + lane % 16;
-      xr[m] = x + (int64_t)(g.list[r < n ? r : n - 1] / k) * d + M::x_offset(lane);
+  const int tiles = I / CT, items = __builtin_amdgcn_readfirstlane(g.n_live) * tiles;
+  const int steps = (d + M::kStep - 1) / M::kStep;
+  int slot = -1, n = 0, e = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int n0 = item % tiles * CT;
+    if (item / tiles != slot) {
+      slot = item / tiles;
+      e = __builtin_amdgcn_readfirstlane(g.live[slot]);
+      n = __builtin_amdgcn_readfirstlane(g.count[e]);
+      few_list(g, P, e);
     }
-    f32x4 acc[C][M::NF];
-    few_stream<M, C, NW>(w, xr, d, 0, steps, wave, lane, acc);
-#pragma unroll
-    for (int m = 0; m < C; ++m) {
-      __syncthreads();   // the buffer's last readers are done
-      few_spill<M>(red, acc[m], wave, lane);
-      __syncthreads();
-      for (int i = tid; i < 16 * CT; i += NT) {
-        const int row = i / CT, c = i % CT, r = r0 + m * 16 + row;
-        if (r >= n) break;   // rows ascend with i
-        const float gate = few_sum<M, NW>(red, row, M::gate_slot(c)), up = few_sum<M, NW>(red, row, M::up_slot(c));
-        few_store(h + (int64_t)g.list[r] * I + n0 + c, gate / (1.f + expf(-gate)) * up);
-      }
-    }
-  });
-}
-
-// ---- down and combine ------------------------------------------------------------
-// grid (column tiles of kCols columns, slots * n_split): slot's expert over
-// the split-th share of I.  Partial rows part[split][pair][d] in float32 go
-// through memory; a device-wide counter a column tile tells the workgroup
-// that finishes last, which adds each token's pairs in slot order (a pair's
-// shares in order before).  Writers release (fence, barrier, then the
-// counter), the last one acquires (counter, barrier, then the fence).
-constexpr int kDnWaves = 4;
-
-template <class M, int MT>
-__global__ __launch_bounds__(kDnWaves * kWave) void k_few_down(
-    const typename M::Act* __restrict__ h, const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
-    int T, int d, int E, int k, int I, typename M::Args wa, int n_split, float* __restrict__ part,
-    int32_t* __restrict__ counters, typename M::Act* __restrict__ out) {
-  constexpr int NW = kDnWaves, NT = NW * kWave, CT = M::kCols;
-  __shared__ FewGroup g;
-  __shared__ float red[NW * 16 * kRedStride<M>];
-  __shared__ int s_last;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int P = T * k, n0 = blockIdx.x * CT, slot = blockIdx.y / n_split, split = blockIdx.y % n_split;
-  const int cols = d - n0 < CT ? d - n0 : CT;
-  for (int p = tid; p < P; p += NT) g.idx[p] = topk_idx[p];
-  const bool work = few_group<NT>(g, P, E, slot);
-  const int n_live = g.n_live;
-  // with no live expert at all, the first workgroup of a column writes its zeros
-  if (!work && (n_live > 0 || blockIdx.y > 0)) return;
-  if (work) {
-    const M w = M::down(wa, __builtin_amdgcn_readfirstlane(g.e), d, I, n0, lane);
-    const int n = __builtin_amdgcn_readfirstlane(g.n), steps = (I + M::kStep - 1) / M::kStep;
-    const int s0 = split * steps / n_split, s1 = (split + 1) * steps / n_split;
+    const M w = M::gate_up(wa, e, d, I, n0, lane);
     few_row_tiles<MT>(n, [&](auto count, int r0) {
       constexpr int C = decltype(count)::value;
-      const typename M::Act* hr[C];
+      const typename M::Act* xr[C];
 #pragma unroll
       for (int m = 0; m < C; ++m) {
         const int r = r0 + m * 16 + lane % 16;
-        hr[m] = h + (int64_t)g.list[r < n ? r : n - 1] * I + M::x_offset(lane);
+        xr[m] = x + (int64_t)(g.list[r < n ? r : n - 1] / k) * d + M::x_offset(lane);
       }
       f32x4 acc[C][M::NF];
-      few_stream<M, C, NW>(w, hr, I, s0, s1, wave, lane, acc);
+      few_stream<M, C, NW>(w, xr, d, 0, steps, wave, lane, acc);
 #pragma unroll
       for (int m = 0; m < C; ++m) {
-        __syncthreads();
+        __syncthreads();   // the buffer's last readers are done
         few_spill<M>(red, acc[m], wave, lane);
         __syncthreads();
         for (int i = tid; i < 16 * CT; i += NT) {
           const int row = i / CT, c = i % CT, r = r0 + m * 16 + row;
-          if (r >= n) break;
-          if (c < cols)
-            part[((int64_t)split * P + g.list[r]) * d + n0 + c] = few_sum<M, NW>(red, row, M::down_slot(c));
+          if (r >= n) break;   // rows ascend with i
+          const float gate = few_sum<M, NW>(red, row, M::gate_slot(c)), up = few_sum<M, NW>(red, row, M::up_slot(c));
+          few_store(h + (int64_t)g.list[r] * I + n0 + c, gate / (1.f + expf(-gate)) * up);
         }
       }
     });
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&counters[blockIdx.x], 1) == n_live * n_split - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
   }
-  for (int i = tid; i < T * (CT / 4); i += NT) {
-    const int t = i / (CT / 4), c = i % (CT / 4) * 4;
-    if (c >= cols) continue;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < k; ++j) {
-      const int p = t * k + j, e = g.idx[p];
-      if (e < 0 || e >= E) continue;
-      const float* yp = part + (int64_t)p * d + n0 + c;
-      f32x4 y = *(const f32x4*)yp;
-      for (int s = 1; s < n_split; ++s) y += *(const f32x4*)(yp + (int64_t)s * P * d);
-      const float wt = topk_w[p];
+}
+
+// ---- down and combine ------------------------------------------------------------
+// Items (live expert, share of I, column tile of kCols columns).  Partial rows
+// part[share][pair][d] in float32 go through memory, and a counter a column
+// tile tells the workgroup that brings the tile's last share, which adds each
+// token's pairs in slot order (a pair's shares in order before).  The partial
+// rows are written and read by device-scope accesses, which pass the XCDs'
+// separate L2s: a workgroup waits until its own are through (vmcnt 0, then the
+// barrier) before it counts.  Device-wide fences in their place flush a whole
+// L2 a workgroup: 98 us instead of 16 for one token of the 128-expert layer.
+template <class M, int MT>
+__global__ __launch_bounds__(M::kDnWaves * kWave, 2) void k_few_down(
+    const typename M::Act* __restrict__ h, const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
+    int T, int d, int E, int k, int I, typename M::Args wa, int n_split, float* __restrict__ part,
+    int32_t* __restrict__ counters, typename M::Act* __restrict__ out) {
+  constexpr int NW = M::kDnWaves, NT = NW * kWave, CT = M::kCols;
+  __shared__ FewGroup g;
+  __shared__ float red[NW * 16 * kRedStride<M>];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int P = T * k, tiles = (d + CT - 1) / CT;
+  for (int p = tid; p < P; p += NT) g.idx[p] = topk_idx[p];
+  few_group<NT>(g, P, E);
+  const int n_live = __builtin_amdgcn_readfirstlane(g.n_live), per = n_split * tiles;
+  // with no live expert at all, one pass over the columns writes zeros
+  const int items = n_live > 0 ? n_live * per : tiles;
+  const int steps = (I + M::kStep - 1) / M::kStep;
+  int slot = -1, n = 0, e = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int tile = item % tiles, split = item / tiles % n_split, n0 = tile * CT;
+    const int cols = d - n0 < CT ? d - n0 : CT;
+    if (n_live > 0) {
+      if (item / per != slot) {
+        slot = item / per;
+        e = __builtin_amdgcn_readfirstlane(g.live[slot]);
+        n = __builtin_amdgcn_readfirstlane(g.count[e]);
+        few_list(g, P, e);
+      }
+      const M w = M::down(wa, e, d, I, n0, lane);
+      const int s0 = split * steps / n_split, s1 = (split + 1) * steps / n_split;
+      few_row_tiles<MT>(n, [&](auto count, int r0) {
+        constexpr int C = decltype(count)::value;
+        const typename M::Act* hr[C];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) sum[v] = fmaf(wt, y[v], sum[v]);
+        for (int m = 0; m < C; ++m) {
+          const int r = r0 + m * 16 + lane % 16;
+          hr[m] = h + (int64_t)g.list[r < n ? r : n - 1] * I + M::x_offset(lane);
+        }
+        f32x4 acc[C][M::NF];
+        few_stream<M, C, NW>(w, hr, I, s0, s1, wave, lane, acc);
+#pragma unroll
+        for (int m = 0; m < C; ++m) {
+          __syncthreads();
+          few_spill<M>(red, acc[m], wave, lane);
+          __syncthreads();
+          for (int i = tid; i < 16 * CT; i += NT) {
+            const int row = i / CT, c = i % CT, r = r0 + m * 16 + row;
+            if (r >= n) break;
+            if (c < cols)
+              __hip_atomic_store(part + ((int64_t)split * P + g.list[r]) * d + n0 + c,
+                                 few_sum<M, NW>(red, row, M::down_slot(c)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+        }
+      });
+      wait_vmcnt<0>();
+      __syncthreads();
+      if (tid == 0)
+        s_last = __hip_atomic_fetch_add(&counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 n_live * n_split - 1;
+      __syncthreads();
+      if (!s_last) continue;
     }
-    few_store4(out + (int64_t)t * d + n0 + c, sum);
+    for (int i = tid; i < T * (CT / 4); i += NT) {
+      const int t = i / (CT / 4), c = i % (CT / 4) * 4;
+      if (c >= cols) continue;
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < k; ++j) {
+        const int p = t * k + j, pe = g.idx[p];
+        if (pe < 0 || pe >= E) continue;
+        const float wt = topk_w[p];
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < n_split; ++s) {
+          const float* yp = part + ((int64_t)s * P + p) * d + n0 + c;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) y[v] += __hip_atomic_load(yp + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[v] = fmaf(wt, y[v], sum[v]);
+      }
+      few_store4(out + (int64_t)t * d + n0 + c, sum);
+    }
   }
 }
 
 // ---- launch ------------------------------------------------------------------------
+
+constexpr int kFewCus = 256, kFewWaves = 16;   // compute units; waves that a workgroup's share of one aims at
 
 // Shares of I in the second kernel: enough workgroups to fill the chip twice,
 // while a wave keeps at least two steps of its own.
@@ -516,7 +550,7 @@ int few_split(int P, int E, int d, int I) {
   const int64_t tiles = ceil_div(d, M::kCols) * (P < E ? P : E);
   const int steps = (int)ceil_div(I, M::kStep);
   int64_t n = ceil_div(512, tiles);
-  const int64_t most = steps / (2 * kDnWaves);
+  const int64_t most = steps / (2 * M::kDnWaves);
   n = n > most ? most : n;
   return (int)(n < 1 ? 1 : n > kFewSplitMax ? kFewSplitMax : n);
 }
@@ -527,25 +561,33 @@ hipError_t few_run(const typename M::Act* x, const float* logits, int T, int d, 
                    typename M::Act* out, const FewScratch& ws, hipStream_t s) {
   const int P = T * k, slots = P < E ? P : E;
   const int tiles = (int)ceil_div(d, M::kCols), n_split = few_split<M>(P, E, d, I);
-  k_few_gate_up<M, MT><<<dim3((unsigned)ceil_div(I, M::kCols / 2), (unsigned)slots), kGuWaves * kWave, 0, s>>>(
+  const int64_t gu_items = (int64_t)slots * (I / (M::kCols / 2)), dn_items = (int64_t)slots * n_split * tiles;
+  const auto grid = [](int64_t items, int waves) {
+    const int64_t most = (int64_t)kFewCus * (kFewWaves / waves);
+    return dim3((unsigned)(items < most ? items : most));
+  };
+  k_few_gate_up<M, MT><<<grid(gu_items, M::kGuWaves), M::kGuWaves * kWave, 0, s>>>(
       x, logits, topk_idx, topk_w, T, d, E, k, I, gu, (typename M::Act*)ws.h, ws.counters, tiles);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_few_down<M, MT><<<dim3((unsigned)tiles, (unsigned)(slots * n_split)), kDnWaves * kWave, 0, s>>>(
+  k_few_down<M, MT><<<grid(dn_items, M::kDnWaves), M::kDnWaves * kWave, 0, s>>>(
       (const typename M::Act*)ws.h, topk_idx, topk_w, T, d, E, k, I, dn, n_split, ws.part, ws.counters, out);
   return hipGetLastError();
 }
 
 // Row tiles held in registers: as many as the tokens can fill, so that an
 // expert's weights are read once (a given pair list may repeat an expert in
-// one token; the kernels then take further rounds).
+// one token; the kernels then take further rounds).  With 8-bit weights two at
+// most: a step has four times the k, and four tiles of it do not fit beside
+// the weights; an expert with more than 32 rows takes two rounds.
 template <class M>
 hipError_t few_dispatch(const typename M::Act* x, const float* logits, int T, int d, int E, int k, int I,
                         typename M::Args gu, typename M::Args dn, int32_t* topk_idx, float* topk_w,
                         typename M::Act* out, const FewScratch& ws, hipStream_t s) {
   if (T <= 16) return few_run<M, 1>(x, logits, T, d, E, k, I, gu, dn, topk_idx, topk_w, out, ws, s);
-  if (T <= 32) return few_run<M, 2>(x, logits, T, d, E, k, I, gu, dn, topk_idx, topk_w, out, ws, s);
-  return few_run<M, 4>(x, logits, T, d, E, k, I, gu, dn, topk_idx, topk_w, out, ws, s);
+  if (T <= 32 || M::kMaxTiles == 2)
+    return few_run<M, 2>(x, logits, T, d, E, k, I, gu, dn, topk_idx, topk_w, out, ws, s);
+  return few_run<M, M::kMaxTiles>(x, logits, T, d, E, k, I, gu, dn, topk_idx, topk_w, out, ws, s);
 }
 
 }  // namespace
@@ -553,7 +595,7 @@ hipError_t few_dispatch(const typename M::Act* x, const float* logits, int T, in
 int few_split_bf16(int P, int E, int d, int I) { return few_split<RowMajor<bf16_t>>(P, E, d, I); }
 int few_split_f32(int P, int E, int d, int I) { return few_split<RowMajor<float>>(P, E, d, I); }
 int few_split_fp8(int P, int E, int d, int I) { return few_split<Blocked8>(P, E, d, I); }
-int few_counters(int d) { return (int)ceil_div(d, 32); }   // the narrowest column tile
+int few_counters(int d) { return (int)ceil_div(d, 64); }   // the narrowest column tile
 
 hipError_t launch_few_bf16(const bf16_t* x, const float* logits, int T, int d, int E, int k, int I, const bf16_t* wgu,
                            const bf16_t* wd, int32_t* topk_idx, float* topk_w, bf16_t* out, const FewScratch& ws,
