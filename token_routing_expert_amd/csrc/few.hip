@@ -37,7 +37,7 @@ template <typename Elem>
 struct RowMajor {
   using Act = Elem;
   static constexpr int V = 16 / (int)sizeof(Elem), NF = V, kStep = 4 * V, kBytes = 16 * V;
-  static constexpr int kGuWaves = 8, kDnWaves = 4, kMaxTiles = 4;
+  static constexpr int kGuWaves = 8, kDnWaves = 8, kMaxTiles = 4;
   static constexpr int kXVec = 1;                     // 16-byte activation loads a row and step
   static constexpr int kCols = 16 * V;                // columns of a tile; gate/up: half gate, half up
   struct Args {
@@ -63,6 +63,7 @@ struct RowMajor {
         row_bytes((int64_t)ld * sizeof(Elem)) {}
 
   __device__ __forceinline__ static int x_offset(int lane) { return lane / 16 * V; }
+  __device__ __forceinline__ static int x_load(int) { return 0; }
   __device__ __forceinline__ static bool x_valid(int, int, int) { return true; }   // K is a multiple of kStep
   __device__ __forceinline__ void load(Regs& g, int step) const {
     const char* p = base + (int64_t)step * kStep * row_bytes;
@@ -105,15 +106,15 @@ struct RowMajor {
 };
 
 // 8-bit [N, K] weights with bf16 activations.  A step is one block of 128
-// columns: lane l loads 32 bytes (k = 32 (l/16) .. +31) of row l % 16 of each
-// fragment, 128 contiguous bytes a row.  e4m3 codes are exact in bf16, so the
-// block's sum comes from bf16 matrix instructions and the scale is applied to
-// it in float32, once a block.  The last block may be half a block: its upper
-// k-groups load nothing and multiply zeros (activations too: what lies behind
-// a row may be a NaN).
+// columns, in two halves of 64: lane l loads 16 bytes (k = 16 (l/16) .. +15 of
+// the half) of row l % 16 of each fragment, 64 contiguous bytes a row.  e4m3
+// codes are exact in bf16, so the block's sum comes from bf16 matrix
+// instructions and the scale is applied to it in float32, once a block.  The
+// last block may be half a block: its upper half is not loaded (activations
+// neither: what lies behind a row may be a NaN) and multiplies zeros.
 struct Blocked8 {
   using Act = bf16_t;
-  static constexpr int NF = 4, kStep = 128, kBytes = 32 * NF;
+  static constexpr int NF = 2, kStep = 128, kBytes = 32 * NF;
   static constexpr int kGuWaves = 4, kDnWaves = 4, kMaxTiles = 2;
   static constexpr int kXVec = 4;
   static constexpr int kCols = 16 * NF;
@@ -128,7 +129,7 @@ struct Blocked8 {
   const uint8_t* base[NF];   // first row of each fragment
   const float* scale[NF];
   uint32_t lane_off;
-  int K, kg;
+  int K;
 
   __device__ __forceinline__ static Blocked8 gate_up(const Args& a, int e, int d, int I, int n0, int lane) {
     Blocked8 m;
@@ -155,24 +156,21 @@ struct Blocked8 {
   }
   __device__ __forceinline__ void set(int k, int lane) {
     K = k;
-    kg = lane / 16 * 32;
-    lane_off = (uint32_t)(lane % 16) * (uint32_t)K + (uint32_t)kg;
+    lane_off = (uint32_t)(lane % 16) * (uint32_t)K + (uint32_t)(lane / 16 * 16);
   }
-  __device__ __forceinline__ static int x_offset(int lane) { return lane / 16 * 32; }
-  __device__ __forceinline__ static bool x_valid(int step, int lane, int K) {
-    return step * kStep + lane / 16 * 32 < K;
-  }
+  // 16-byte activation load c of a step: k = 64 (c / 2) + 16 (l / 16) + 8 (c % 2)
+  __device__ __forceinline__ static int x_offset(int lane) { return lane / 16 * 16; }
+  __device__ __forceinline__ static int x_load(int c) { return c / 2 * 64 + c % 2 * 8; }
+  __device__ __forceinline__ static bool x_valid(int step, int c, int K) { return c < 2 || step * kStep + 64 < K; }
   __device__ __forceinline__ void load(Regs& g, int step) const {
-    const bool in = step * kStep + kg < K;
+    const bool whole = step * kStep + 64 < K;
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const uint8_t* p = base[f] + (int64_t)step * kStep;
+      const uint8_t* p = base[f] + (int64_t)step * kStep + lane_off;
       g.s[f] = scale[f][step];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        g.r[f][h] = u32x4{0, 0, 0, 0};
-        if (in) g.r[f][h] = __builtin_nontemporal_load((const u32x4*)(p + lane_off + 16 * h));
-      }
+      g.r[f][0] = *(const u32x4*)p;
+      g.r[f][1] = u32x4{0, 0, 0, 0};
+      if (whole) g.r[f][1] = *(const u32x4*)(p + 64);
     }
   }
   __device__ __forceinline__ static bf16x8 widen(uint32_t lo, uint32_t hi) {
@@ -306,10 +304,9 @@ __device__ __forceinline__ void few_route(const float* __restrict__ logits, int 
 template <class M, int C, int NW>
 __device__ __forceinline__ void few_stream(const M& w, const typename M::Act* const (&x)[C], int K, int s0, int s1,
                                            int wave, int lane, f32x4 (&acc)[C][M::NF]) {
-  using Act = typename M::Act;
-  // steps loaded together: 256 bytes of weights a lane, fewer with more row
+  // steps loaded together: 128 bytes of weights a lane, fewer with more row
   // tiles (their sums and activations need the registers)
-  constexpr int U0 = 256 / M::kBytes / C, U = U0 > 0 ? U0 : 1, XE = 16 / (int)sizeof(Act);
+  constexpr int U0 = 128 / M::kBytes / C, U = U0 > 0 ? U0 : 1;
 #pragma unroll
   for (int m = 0; m < C; ++m)
 #pragma unroll
@@ -323,13 +320,12 @@ __device__ __forceinline__ void few_stream(const M& w, const typename M::Act* co
       const int s = st + u * NW;
       if (s >= s1) break;
       w.load(g[u], s);
-      const bool ok = M::x_valid(s, lane, K);
 #pragma unroll
       for (int m = 0; m < C; ++m)
 #pragma unroll
         for (int c = 0; c < M::kXVec; ++c) {
           xr[u][m][c] = u32x4{0, 0, 0, 0};
-          if (ok) xr[u][m][c] = *(const u32x4*)(x[m] + (int64_t)s * M::kStep + c * XE);
+          if (M::x_valid(s, c, K)) xr[u][m][c] = *(const u32x4*)(x[m] + (int64_t)s * M::kStep + M::x_load(c));
         }
     }
 #pragma unroll
@@ -541,15 +537,16 @@ __global__ __launch_bounds__(M::kDnWaves * kWave, 2) void k_few_down(
 
 // ---- launch ------------------------------------------------------------------------
 
-constexpr int kFewCus = 256, kFewWaves = 16;   // compute units; waves that a workgroup's share of one aims at
+constexpr int kFewCus = 256, kFewWaves = 16;   // compute units, and waves that one holds at these register counts
 
-// Shares of I in the second kernel: enough workgroups to fill the chip twice,
-// while a wave keeps at least two steps of its own.
+// Shares of I in the second kernel: 128 workgroups at least (of 8 waves; every
+// further share is a partial row more to write, wait for and read), while a
+// wave keeps two steps of its own.
 template <class M>
 int few_split(int P, int E, int d, int I) {
   const int64_t tiles = ceil_div(d, M::kCols) * (P < E ? P : E);
   const int steps = (int)ceil_div(I, M::kStep);
-  int64_t n = ceil_div(512, tiles);
+  int64_t n = ceil_div(128, tiles);
   const int64_t most = steps / (2 * M::kDnWaves);
   n = n > most ? most : n;
   return (int)(n < 1 ? 1 : n > kFewSplitMax ? kFewSplitMax : n);
@@ -563,7 +560,7 @@ hipError_t few_run(const typename M::Act* x, const float* logits, int T, int d, 
   const int tiles = (int)ceil_div(d, M::kCols), n_split = few_split<M>(P, E, d, I);
   const int64_t gu_items = (int64_t)slots * (I / (M::kCols / 2)), dn_items = (int64_t)slots * n_split * tiles;
   const auto grid = [](int64_t items, int waves) {
-    const int64_t most = (int64_t)kFewCus * (kFewWaves / waves);
+    const int64_t most = (int64_t)kFewCus * ((kFewWaves + waves - 1) / waves);
     return dim3((unsigned)(items < most ? items : most));
   };
   k_few_gate_up<M, MT><<<grid(gu_items, M::kGuWaves), M::kGuWaves * kWave, 0, s>>>(
@@ -595,7 +592,7 @@ hipError_t few_dispatch(const typename M::Act* x, const float* logits, int T, in
 int few_split_bf16(int P, int E, int d, int I) { return few_split<RowMajor<bf16_t>>(P, E, d, I); }
 int few_split_f32(int P, int E, int d, int I) { return few_split<RowMajor<float>>(P, E, d, I); }
 int few_split_fp8(int P, int E, int d, int I) { return few_split<Blocked8>(P, E, d, I); }
-int few_counters(int d) { return (int)ceil_div(d, 64); }   // the narrowest column tile
+int few_counters(int d) { return (int)ceil_div(d, 32); }   // the narrowest column tile
 
 hipError_t launch_few_bf16(const bf16_t* x, const float* logits, int T, int d, int E, int k, int I, const bf16_t* wgu,
                            const bf16_t* wd, int32_t* topk_idx, float* topk_w, bf16_t* out, const FewScratch& ws,
