@@ -34,7 +34,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads8 = 512, kBN = 256, kStageK = 128;
-constexpr int kXcds = 8;                         // workgroups are dealt round-robin over the XCDs
+constexpr int kCus = 256, kXcds = 8;             // workgroups are dealt round-robin over the XCDs
 constexpr int kGroupM = 8;                       // row tiles of a weight slice that run together
 constexpr uint32_t kPark = 0x80000000u;          // past every buffer: reads zeros
 
@@ -65,22 +65,36 @@ template <int BM>
 struct Stage8 {
   uint8_t a[BM * kStageK];
   uint8_t b[kBN * kStageK];
-  float as[BM < 64 ? 64 : BM];
+  float as[(BM + 63) / 64 * 64];   // whole loads of 64
   float bs[64];              // [0], [1]: the tile's two weight blocks
 };
 
-// 32 bytes of k for one row of an operand: chunks q and q + 4 of the row (the
-// same k for both operands, in an order of no consequence to the sum).
-__device__ __forceinline__ i32x8 operand8(const uint8_t* tile, int row, int q) {
-  const uint8_t* p = tile + row * kStageK + ((q ^ (row & 7)) * 16);
-  const u32x4 lo = *(const u32x4*)p, hi = *(const u32x4*)(tile + row * kStageK + (((q + 4) ^ (row & 7)) * 16));
-  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+// 32 bytes of k of an operand row, chunks q and q + 4 (the same k for both
+// operands, in an order of no consequence to the sum): `lo` and `hi` are the
+// lane's places of the two in the first 16 rows, `at` the rows' distance.
+__device__ __forceinline__ i32x8 operand8(const uint8_t* lo, const uint8_t* hi, int at) {
+  const u32x4 a = *(const u32x4*)(lo + at), b = *(const u32x4*)(hi + at);
+  return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
 __device__ __forceinline__ f32x4 mfma8(i32x8 a, i32x8 b) {
   // both operands e4m3 (format 0); zero scale operands select the form without scales
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
+
+// The same number, which the compiler takes for a new one: what is derived from
+// it inside a loop is computed there, not kept in registers across the loop.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// What a tile is: `rows` rows from row0 on, of expert e, times its weights from
+// output column n0 on.
+struct Tile8 {
+  int e, n0, rows;
+  int64_t row0;
+};
 
 template <bool GATE_UP, int BM, int WM>
 __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
@@ -89,116 +103,132 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   constexpr int A_LOADS = BM / 8, B_LOADS = kBN / 8;   // 1 KB loads of a stage
   constexpr int A_PER = (A_LOADS + NW - 1) / NW, B_PER = B_LOADS / NW;
   __shared__ __attribute__((aligned(1024))) Stage8<BM> st[2];
-  __shared__ int s_tiles[kMaxExperts];
-  __shared__ int s_found[4];
-  __shared__ int s_total;
+  __shared__ int s_tiles[kMaxExperts];    // row tiles of the experts up to and with this one
+  __shared__ int s_wave[4];
+  __shared__ int s_found[2][3];           // expert, row tile, column tile
+  __shared__ int s_rows[BM];              // rows behind the next tile's rows, or -1
+  __shared__ uint32_t s_amax[GATE_UP ? WN * BM : 1];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n_tiles = (g.N + TN - 1) / TN;
 
-  // ---- which tile: experts' row tiles counted from the offsets
-  if (tid < kMaxExperts) {
+  // ---- the experts' row tiles, counted from the offsets
+  {
     int n = 0;
     if (tid < g.E) {
       const int64_t r0 = clampi<int64_t>(g.offsets[tid], 0, g.max_rows);
       const int64_t r1 = clampi<int64_t>(g.offsets[tid + 1], r0, g.max_rows);
       n = (int)((r1 - r0 + BM - 1) / BM);
     }
-    // inclusive scan over the experts: in the wave, then over the four waves
+    // inclusive scan: in the wave, then over the four waves of experts
     int x = n;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
       const int y = __shfl_up(x, off, kWave);
       if (lane >= off) x += y;
     }
-    s_tiles[tid] = x;
-  }
-  __syncthreads();
-  int before = 0;
-  if (tid < kMaxExperts) {
-    for (int w = 0; w < wave; ++w) before += s_tiles[w * kWave + kWave - 1];
-    if (tid == kMaxExperts - 1) s_total = before + s_tiles[tid];
-  }
-  __syncthreads();
-  const int64_t total = (int64_t)s_total * n_tiles, per = (total + kXcds - 1) / kXcds;
-  const int64_t mine = blockIdx.x / kXcds, tile = (blockIdx.x % kXcds) * per + mine;
-  if (mine >= per || tile >= total) return;
-  if (tid < kMaxExperts) {
-    const int64_t hi = (int64_t)(before + s_tiles[tid]) * n_tiles;
-    const int64_t lo = (int64_t)(before + (lane ? s_tiles[tid - 1] : 0)) * n_tiles;
-    if (tile >= lo && tile < hi) {
-      const int m_tiles = (int)((hi - lo) / n_tiles), at = (int)(tile - lo);
-      const int group = at / (kGroupM * n_tiles), in = at - group * (kGroupM * n_tiles);
-      const int wide = m_tiles - group * kGroupM < kGroupM ? m_tiles - group * kGroupM : kGroupM;
-      s_found[0] = tid;
-      s_found[1] = group * kGroupM + in % wide;
-      s_found[2] = in / wide;
+    if (wave < 4 && lane == kWave - 1) s_wave[wave] = x;
+    __syncthreads();
+    if (wave < 4) {
+      for (int w = 0; w < wave; ++w) x += s_wave[w];
+      s_tiles[tid] = x;
     }
+    __syncthreads();
   }
-  __syncthreads();
-  const int e = __builtin_amdgcn_readfirstlane(s_found[0]), mt = __builtin_amdgcn_readfirstlane(s_found[1]),
-            n0 = __builtin_amdgcn_readfirstlane(s_found[2]) * TN;
-  const int64_t first = clampi<int64_t>(g.offsets[e], 0, g.max_rows);
-  const int64_t last = clampi<int64_t>(g.offsets[e + 1], first, g.max_rows);
-  const int64_t row0 = first + (int64_t)mt * BM;
-  const int rows = (int)(last - row0 < BM ? last - row0 : BM);
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(s_tiles[kMaxExperts - 1]) * n_tiles;
+  // this XCD's share of the tiles, and this workgroup's walk through it
+  const int64_t per = (total + kXcds - 1) / kXcds, x0 = (blockIdx.x % kXcds) * per;
+  const int64_t x1 = x0 + per < total ? x0 + per : total;
+  const int64_t stride = gridDim.x / kXcds;
 
-  // ---- operands
   const int K = g.K, KB = (K + 127) / 128, steps = KB;
+  const int NB = (g.N + 127) / 128;
   const bool tail = K % 128 != 0;                    // the last stage has half a block
   const int chunk = (lane & 7) ^ (lane >> 3);        // the 16 bytes of a row this lane loads
   const bool gather = g.row_token != nullptr;
-  const uint8_t* a_base = gather ? g.a : g.a + row0 * K;
-  const float* as_base = gather ? g.a_s : g.a_s + row0 * KB;
-  const int64_t a_span = gather ? g.a_rows : rows;
-  const __amdgpu_buffer_rsrc_t a_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(a_base), (short)0, (int)(a_span * K), kBufferConfig);
-  const __amdgpu_buffer_rsrc_t as_rsrc =
-      __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(as_base), (short)0, (int)(a_span * KB * 4), kBufferConfig);
-  const int64_t w_rows = GATE_UP ? 2 * (int64_t)g.N : g.N;
-  const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      uniform_ptr(g.w + e * w_rows * K), (short)0, (int)(w_rows * K), kBufferConfig);
-  const int NB = (g.N + 127) / 128;
-  const int64_t ws_rows = GATE_UP ? 2 * NB : NB;
-  const __amdgpu_buffer_rsrc_t ws_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      uniform_ptr(g.w_s + e * ws_rows * KB), (short)0, (int)(ws_rows * KB * 4), kBufferConfig);
-  // row of `a` behind the tile's row r, or -1
-  auto source_row = [&](int r) -> int64_t {
-    if (r >= rows) return -1;
-    if (!gather) return r;
-    const int64_t t = g.row_token[row0 + r];
-    MOE_DCHECK(t >= 0 && t < g.a_rows);
-    return t >= 0 && t < g.a_rows ? t : -1;
-  };
-  uint32_t a_off[A_PER], b_off[B_PER], as_off = kPark, bs_off = kPark;
-#pragma unroll
-  for (int p = 0; p < A_PER; ++p) {
-    const int i = wave + NW * p;
-    const int64_t r = i < A_LOADS ? source_row(8 * i + lane / 8) : -1;
-    a_off[p] = r < 0 ? kPark : (uint32_t)(r * K + chunk * 16);
-  }
-#pragma unroll
-  for (int p = 0; p < B_PER; ++p) {
-    const int r = 8 * (wave + NW * p) + lane / 8;
-    int64_t src;
-    if constexpr (GATE_UP) {
-      const int col = n0 + r / BW * (BW / 2) + r % (BW / 2);
-      src = col < g.N ? (int64_t)(r % BW / (BW / 2)) * g.N + col : -1;
-    } else {
-      src = n0 + r < g.N ? n0 + r : -1;
+  const int64_t w_rows = GATE_UP ? 2 * (int64_t)g.N : g.N, ws_rows = GATE_UP ? 2 * NB : NB;
+
+  // Finds a tile's expert and place; `which` alternates.  One thread writes,
+  // everyone reads after the next barrier.
+  auto find = [&](int64_t tile, int which) {
+    if (tid < kMaxExperts) {
+      const int64_t hi = (int64_t)s_tiles[tid] * n_tiles, lo = tid ? (int64_t)s_tiles[tid - 1] * n_tiles : 0;
+      if (tile >= lo && tile < hi) {
+        const int m_tiles = (int)((hi - lo) / n_tiles), at = (int)(tile - lo);
+        const int group = at / (kGroupM * n_tiles), in = at - group * (kGroupM * n_tiles);
+        const int wide = m_tiles - group * kGroupM < kGroupM ? m_tiles - group * kGroupM : kGroupM;
+        s_found[which][0] = tid;
+        s_found[which][1] = group * kGroupM + in % wide;
+        s_found[which][2] = in / wide;
+      }
     }
-    b_off[p] = src < 0 ? kPark : (uint32_t)(src * K + chunk * 16);
-  }
+  };
+  auto found = [&](int which) {
+    Tile8 t;
+    t.e = __builtin_amdgcn_readfirstlane(s_found[which][0]);
+    t.n0 = __builtin_amdgcn_readfirstlane(s_found[which][2]) * TN;
+    const int64_t first = clampi<int64_t>(g.offsets[t.e], 0, g.max_rows);
+    const int64_t last = clampi<int64_t>(g.offsets[t.e + 1], first, g.max_rows);
+    t.row0 = first + (int64_t)__builtin_amdgcn_readfirstlane(s_found[which][1]) * BM;
+    t.rows = (int)(last - t.row0 < BM ? last - t.row0 : BM);
+    return t;
+  };
+  auto fetch_rows = [&](const Tile8& t) {   // into s_rows
+    if (gather && tid < BM) {
+      int64_t src = -1;
+      if (tid < t.rows) {
+        src = g.row_token[t.row0 + tid];
+        MOE_DCHECK(src >= 0 && src < g.a_rows);
+        src = src >= 0 && src < g.a_rows ? src : -1;
+      }
+      s_rows[tid] = (int)src;
+    }
+  };
+
+  // ---- the operands of the tile whose stages are being loaded
+  __amdgpu_buffer_rsrc_t a_rsrc, as_rsrc, w_rsrc, ws_rsrc;
+  uint32_t a_off[A_PER], b_off[B_PER], as_off = kPark, bs_off = kPark;
   constexpr int AS_WAVES = (BM + 63) / 64;
-  if (wave < AS_WAVES) {
-    const int64_t r = wave * 64 + lane < BM ? source_row(wave * 64 + lane) : -1;
-    as_off = r < 0 ? kPark : (uint32_t)(r * KB * 4);
-  }
-  if (wave == NW - 1 && lane < 2) {
-    const int64_t b = GATE_UP ? (int64_t)lane * NB + n0 / 128 : n0 / 128 + lane;
-    bs_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
-  }
-  auto issue = [&](int step) {
-    Stage8<BM>* s = &st[step & 1];
+  auto aim = [&](const Tile8& t) {
+    const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
+    const int64_t a_span = gather ? g.a_rows : t.rows;
+    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * K), (short)0,
+                                               (int)(a_span * K), kBufferConfig);
+    as_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a_s : g.a_s + t.row0 * KB), (short)0,
+                                                (int)(a_span * KB * 4), kBufferConfig);
+    w_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w + t.e * w_rows * K), (short)0, (int)(w_rows * K),
+                                               kBufferConfig);
+    ws_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w_s + t.e * ws_rows * KB), (short)0,
+                                                (int)(ws_rows * KB * 4), kBufferConfig);
+    auto source_row = [&](int r) { return r >= t.rows ? -1 : gather ? s_rows[r] : r; };
+#pragma unroll
+    for (int p = 0; p < A_PER; ++p) {
+      const int i = wave + NW * p;
+      const int r = i < A_LOADS ? source_row(8 * i + ln / 8) : -1;
+      a_off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)K + piece;
+    }
+#pragma unroll
+    for (int p = 0; p < B_PER; ++p) {
+      const int r = 8 * (wave + NW * p) + ln / 8;
+      int64_t src;
+      if constexpr (GATE_UP) {
+        const int col = t.n0 + r / BW * (BW / 2) + r % (BW / 2);
+        src = col < g.N ? (int64_t)(r % BW / (BW / 2)) * g.N + col : -1;
+      } else {
+        src = t.n0 + r < g.N ? t.n0 + r : -1;
+      }
+      b_off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
+    }
+    if (wave < AS_WAVES) {
+      const int r = wave * 64 + ln < BM ? source_row(wave * 64 + ln) : -1;
+      as_off = r < 0 ? kPark : (uint32_t)r * (uint32_t)(KB * 4);
+    }
+    if (wave == NW - 1 && ln < 2) {
+      const int64_t b = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
+      bs_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
+    }
+  };
+  auto issue = [&](int step, int buf) {
+    Stage8<BM>* s = &st[buf];
     const bool cut = tail && step == steps - 1 && chunk >= 4;
 #pragma unroll
     for (int p = 0; p < B_PER; ++p)
@@ -213,114 +243,161 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 
   // ---- the products
   const int wm = wave % WM, wn = wave / WM, q = lane / 16, l16 = lane % 16;
-  const int frags = (rows + 15) / 16;
-  const int live = frags > wm ? (frags - wm + WM - 1) / WM : 0;   // this wave's fragments that hold rows
+  const int place = l16 * kStageK + ((q ^ (l16 & 7)) * 16);   // rows are 16 apart: l16 & 7 is row & 7
   f32x4 acc[MF][NF];
-#pragma unroll
-  for (int m = 0; m < MF; ++m)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the weights' fragments stay in registers, the rows' go by
   auto multiply = [&](auto count, const Stage8<BM>& s) {
     constexpr int M = decltype(count)::value;
-    i32x8 x[M];
-    float sc[M][2];
     const float s0 = GATE_UP ? s.bs[0] : s.bs[wn * BW / 128], s1 = GATE_UP ? s.bs[1] : 0.f;
+    const uint8_t *a_lo = s.a + wm * 16 * kStageK + place, *a_hi = s.a + wm * 16 * kStageK + (place ^ 64);
+    const uint8_t *b_lo = s.b + wn * BW * kStageK + place, *b_hi = s.b + wn * BW * kStageK + (place ^ 64);
+    const float* as = s.as + wm * 16 + l16;
+    i32x8 w[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) w[f] = operand8(b_lo, b_hi, f * 16 * kStageK);
+    // row fragment m multiplies while m + 1 is read; the scheduling barriers
+    // keep the compiler from reading all fragments ahead, which no register is
+    // left for
+    i32x8 x[2];
+    float xs[2];
+    x[0] = operand8(a_lo, a_hi, 0);
+    xs[0] = as[0];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const int r = (m * WM + wm) * 16 + l16;
-      x[m] = operand8(s.a, r, q);
-      const float as = s.as[r];
-      sc[m][0] = as * s0;
-      sc[m][1] = GATE_UP ? as * s1 : 0.f;
-    }
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 part[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const i32x8 w = operand8(s.b, wn * BW + f * 16 + l16, q);
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const f32x4 part = mfma8(w, x[m]);
-        const float c = sc[m][GATE_UP && f >= NF / 2 ? 1 : 0];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[m][f][v] = fmaf(c, part[v], acc[m][f][v]);
+      for (int f = 0; f < NF; ++f) part[f] = mfma8(w[f], x[m & 1]);
+      if (m + 1 < M) {
+        x[(m + 1) & 1] = operand8(a_lo, a_hi, (m + 1) * WM * 16 * kStageK);
+        xs[(m + 1) & 1] = as[(m + 1) * WM * 16];
       }
-    }
-  };
-  auto loop = [&](auto count) {
-    for (int step = 0; step < steps; ++step) {
-      // this wave's loads of the stage have landed and its reads of the other
-      // buffer have returned (vmcnt and lgkmcnt 0); with the barrier, everyone's
-      __builtin_amdgcn_s_waitcnt(7 << 4);
-      stage_barrier();
-      if (step + 1 < steps) issue(step + 1);
-      if constexpr (decltype(count)::value > 0) multiply(count, st[step & 1]);
-    }
-  };
-  issue(0);
-  if (live >= MF) loop(Count<MF>{});
-  else if (MF > 3 && live == 3) loop(Count<(MF > 3 ? 3 : 0)>{});
-  else if (MF > 2 && live == 2) loop(Count<(MF > 2 ? 2 : 0)>{});
-  else if (MF > 1 && live == 1) loop(Count<(MF > 1 ? 1 : 0)>{});
-  else loop(Count<0>{});
-
-  // ---- results: lane has columns 4 q .. +3 of each fragment, of row l16
-  if constexpr (GATE_UP) {
-    uint32_t* s_amax = (uint32_t*)st[0].a;   // [WN][BM]
-    __syncthreads();                          // the stages' readers are done
-    uint32_t top[MF];
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      top[m] = 0;
-      if (m < live) {
-#pragma unroll
-        for (int f = 0; f < NF / 2; ++f)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float gate = acc[m][f][v], h = gate / (1.f + expf(-gate)) * acc[m][f + NF / 2][v];
-            acc[m][f][v] = h;
-            top[m] = abs_bits(h) > top[m] ? abs_bits(h) : top[m];
-          }
-#pragma unroll
-        for (int off = 16; off < kWave; off <<= 1) {
-          const uint32_t o = __shfl_xor(top[m], off, kWave);
-          top[m] = o > top[m] ? o : top[m];
-        }
-        if (q == 0) s_amax[wn * BM + (m * WM + wm) * 16 + l16] = top[m];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      const int r = (m * WM + wm) * 16 + l16;
-      if (m >= live || r >= rows) continue;
-      uint32_t t = 0;
-#pragma unroll
-      for (int w = 0; w < WN; ++w) t = s_amax[w * BM + r] > t ? s_amax[w * BM + r] : t;
-      float scale, inv;
-      bool finite;
-      power_scale(t, scale, inv, finite);
-      if (wn == 0 && q == 0) g.out_s[(row0 + r) * NB + n0 / 128] = scale;
-      uint8_t* o = (uint8_t*)g.out + (row0 + r) * g.N;
-#pragma unroll
-      for (int f = 0; f < NF / 2; ++f) {
-        const int col = n0 + wn * (BW / 2) + f * 16 + q * 4;
-        const uint32_t c = pack_fp8x4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv, acc[m][f][3] * inv);
-        if (col < g.N) *(uint32_t*)(o + col) = finite ? c : kNan8;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      const int r = (m * WM + wm) * 16 + l16;
-      if (m >= live || r >= rows) continue;
-      bf16_t* o = (bf16_t*)g.out + (row0 + r) * g.N;
+      const float c0 = xs[m & 1] * s0, c1 = xs[m & 1] * s1;
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const int col = n0 + wn * BW + f * 16 + q * 4;
-        if (col < g.N)
-          *(uint2*)(o + col) = make_uint2(pack_bf16x2(acc[m][f][0], acc[m][f][1]),
-                                          pack_bf16x2(acc[m][f][2], acc[m][f][3]));
+        const float c = GATE_UP && f >= NF / 2 ? c1 : c0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[m][f][v] = fmaf(c, part[f][v], acc[m][f][v]);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int64_t tile = x0 + blockIdx.x / kXcds;
+  if (tile >= x1) return;
+  find(tile, 0);
+  __syncthreads();
+  Tile8 t = found(0);
+  fetch_rows(t);
+  __syncthreads();
+  aim(t);
+  issue(0, 0);
+  int buf = 0, which = 0;
+  while (true) {
+    const int frags = (t.rows + 15) / 16;
+    const int live = frags > wm ? (frags - wm + WM - 1) / WM : 0;   // this wave's fragments that hold rows
+    const bool more = tile + stride < x1;
+    Tile8 next = t;
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto walk = [&](auto count) {
+      for (int step = 0; step < steps; ++step) {
+        // this wave's loads of the stage have landed and its reads of the
+        // other buffer have returned (vmcnt and lgkmcnt 0); with the barrier,
+        // everyone's
+        __builtin_amdgcn_s_waitcnt(7 << 4);
+        stage_barrier();
+        if (step + 1 < steps) issue(step + 1, buf ^ 1);
+        // the next tile's place is found behind the first stage's barrier, and
+        // its first stage loads while this tile's last one multiplies
+        if (step == 0 && more) {
+          find(tile + stride, which ^ 1);
+          lds_barrier();
+          next = found(which ^ 1);
+          fetch_rows(next);
+        }
+        if (step + 1 == steps && more) {
+          if (steps == 1) lds_barrier();
+          aim(next);
+          issue(0, buf ^ 1);
+        }
+        if constexpr (decltype(count)::value > 0) multiply(count, st[buf]);
+        buf ^= 1;
+      }
+    };
+    // as many fragments as hold rows, in steps of two (one without rows is
+    // zeros in the stage)
+    if (live > 8) walk(Count<MF>{});
+    else if (live > 6) walk(Count<(MF < 8 ? MF : 8)>{});
+    else if (live > 4) walk(Count<(MF < 6 ? MF : 6)>{});
+    else if (live > 2) walk(Count<(MF < 4 ? MF : 4)>{});
+    else if (live > 0) walk(Count<(MF < 2 ? MF : 2)>{});
+    else walk(Count<0>{});
+
+    // ---- results: lane has columns 4 eq .. +3 of each fragment, of row er
+    const int eq = fresh(lane) / 16, er = fresh(lane) % 16;
+    if constexpr (GATE_UP) {
+      uint32_t top[MF];
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        top[m] = 0;
+        if (m < live) {
+#pragma unroll
+          for (int f = 0; f < NF / 2; ++f)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float gate = acc[m][f][v], h = gate / (1.f + expf(-gate)) * acc[m][f + NF / 2][v];
+              acc[m][f][v] = h;
+              top[m] = abs_bits(h) > top[m] ? abs_bits(h) : top[m];
+            }
+#pragma unroll
+          for (int off = 16; off < kWave; off <<= 1) {
+            const uint32_t o = __shfl_xor(top[m], off, kWave);
+            top[m] = o > top[m] ? o : top[m];
+          }
+          if (eq == 0) s_amax[wn * BM + (m * WM + wm) * 16 + er] = top[m];
+        }
+      }
+      lds_barrier();   // (not a full one: the next tile's stage is on its way)
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int r = (m * WM + wm) * 16 + er;
+        if (m >= live || r >= t.rows) continue;
+        uint32_t a = 0;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) a = s_amax[w * BM + r] > a ? s_amax[w * BM + r] : a;
+        float scale, inv;
+        bool finite;
+        power_scale(a, scale, inv, finite);
+        if (wn == 0 && eq == 0) g.out_s[(t.row0 + r) * NB + t.n0 / 128] = scale;
+        uint8_t* o = (uint8_t*)g.out + (t.row0 + r) * g.N;
+#pragma unroll
+        for (int f = 0; f < NF / 2; ++f) {
+          const int col = t.n0 + wn * (BW / 2) + f * 16 + eq * 4;
+          const uint32_t c = pack_fp8x4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv, acc[m][f][3] * inv);
+          if (col < g.N) *(uint32_t*)(o + col) = finite ? c : kNan8;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        const int r = (m * WM + wm) * 16 + er;
+        if (m >= live || r >= t.rows) continue;
+        bf16_t* o = (bf16_t*)g.out + (t.row0 + r) * g.N;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const int col = t.n0 + wn * BW + f * 16 + eq * 4;
+          if (col < g.N)
+            *(uint2*)(o + col) = make_uint2(pack_bf16x2(acc[m][f][0], acc[m][f][1]),
+                                            pack_bf16x2(acc[m][f][2], acc[m][f][3]));
+        }
+      }
+    }
+    if (!more) return;
+    tile += stride;
+    which ^= 1;
+    t = next;
   }
 }
 
@@ -329,7 +406,8 @@ hipError_t gemm8(const Gemm8Args& g, hipStream_t s) {
   // every expert may leave one partly filled tile
   const int64_t m_tiles = g.max_rows / BM + (g.max_rows < g.E ? g.max_rows : g.E);
   const int64_t tiles = m_tiles * ceil_div(g.N, GATE_UP ? kBN / 2 : kBN);
-  k_gemm8<GATE_UP, BM, WM><<<(unsigned)round_up(tiles, kXcds), kThreads8, 0, s>>>(g);
+  const int64_t most = kCus * (2 * sizeof(Stage8<BM>) * 2 < 150 * 1024 ? 2 : 1);   // resident workgroups, by LDS
+  k_gemm8<GATE_UP, BM, WM><<<(unsigned)(tiles < most ? round_up(tiles, kXcds) : most), kThreads8, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -342,7 +420,7 @@ hipError_t gemm8_any(const Gemm8Args& g, hipStream_t s) {
   if (want <= 32) return gemm8<GATE_UP, 32, 1>(g, s);
   if (want <= 64) return gemm8<GATE_UP, 64, 1>(g, s);
   if (want <= 128) return gemm8<GATE_UP, 128, 2>(g, s);
-  return gemm8<GATE_UP, 256, 4>(g, s);
+  return gemm8<GATE_UP, 288, 2>(g, s);
 }
 
 }  // namespace
