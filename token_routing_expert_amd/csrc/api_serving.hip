@@ -60,6 +60,15 @@ moe_status check_few(const void* x, const float* logits, int32_t T, int32_t d, i
 // Row scales of `cols` columns.
 size_t scale_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * ceil_div(cols, 128)) * 4; }
 
+// Bytes between rows of 8-bit codes in a workspace: whole cache lines, where
+// that keeps the array's offsets below 2^31 (the caller's own arrays are
+// dense; 2880 columns are 22.5 lines, and every other row's loads then take
+// two halves for each line: the 128-expert layer's products are 8% slower).
+int row_bytes8(int64_t rows, int64_t cols) {
+  const int64_t padded = round_up(cols, 128);
+  return (int)(rows * padded < kMaxElems ? padded : cols);
+}
+
 // Byte layout of moe_grouped_ffn_fp8's workspace: h in codes and scales.
 struct Ffn8Layout {
   size_t h_q, h_s, total;
@@ -68,7 +77,7 @@ struct Ffn8Layout {
 Ffn8Layout ffn8_layout(int64_t rows, int64_t I) {
   Ffn8Layout L;
   size_t o = 0;
-  L.h_q = o; o += align256((size_t)(rows * I));
+  L.h_q = o; o += align256((size_t)(rows * row_bytes8(rows, I)));
   L.h_s = o; o += align256(scale_bytes(rows, I));
   L.total = o;
   return L;
@@ -83,7 +92,7 @@ Forward8Layout forward8_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64
   const int64_t P = T * k;
   Forward8Layout L;
   size_t o = 0;
-  L.x_q = o;       o += align256((size_t)(T * d));
+  L.x_q = o;       o += align256((size_t)(T * row_bytes8(T, d)));
   L.x_s = o;       o += align256(scale_bytes(T, d));
   L.pair_row = o;  o += align256((size_t)P * 4);
   L.row_token = o; o += align256((size_t)P * 4);
@@ -120,8 +129,8 @@ moe_status moe_quantize_rows(const void* x, moe_dtype dt, int32_t rows, int32_t 
   if (!x || !q || !scale || !aligned16(x, q)) return MOE_ERR_ARG;
   hipStream_t s = (hipStream_t)stream;
   if (dt == MOE_BF16)
-    return from_hip(launch_quantize_rows_bf16((const bf16_t*)x, rows, cols, (uint8_t*)q, scale, s));
-  return from_hip(launch_quantize_rows_f32((const float*)x, rows, cols, (uint8_t*)q, scale, s));
+    return from_hip(launch_quantize_rows_bf16((const bf16_t*)x, rows, cols, (uint8_t*)q, cols, scale, s));
+  return from_hip(launch_quantize_rows_f32((const float*)x, rows, cols, (uint8_t*)q, cols, scale, s));
 }
 
 moe_status moe_quantize_weights(const void* w_gate_up, const void* w_down, moe_dtype dt, int32_t E, int32_t d,
@@ -152,9 +161,9 @@ moe_status moe_gate_up_swiglu_fp8(const void* x_q, const float* x_s, const int32
   if (!expert_offsets || !w_gate_up_q || !w_gate_up_s || !h_q || !h_s) return MOE_ERR_ARG;
   if (!x_q || !x_s) return MOE_ERR_ARG;
   if (!aligned16(x_q, w_gate_up_q, h_q)) return MOE_ERR_ARG;
-  return from_hip(launch_gate_up_fp8((const uint8_t*)x_q, x_s, expert_offsets, max_rows, E, d, I,
-                                     (const uint8_t*)w_gate_up_q, w_gate_up_s, row_token, x_rows, (uint8_t*)h_q, h_s,
-                                     (hipStream_t)stream));
+  return from_hip(launch_gate_up_fp8((const uint8_t*)x_q, d, x_s, expert_offsets, max_rows, E, d, I,
+                                     (const uint8_t*)w_gate_up_q, w_gate_up_s, row_token, x_rows, (uint8_t*)h_q, I,
+                                     h_s, (hipStream_t)stream));
 }
 
 moe_status moe_down_proj_fp8(const void* h_q, const float* h_s, const int32_t* expert_offsets, int32_t max_rows,
@@ -164,7 +173,7 @@ moe_status moe_down_proj_fp8(const void* h_q, const float* h_s, const int32_t* e
   if (max_rows == 0) return MOE_OK;
   if (!h_q || !h_s || !expert_offsets || !w_down_q || !w_down_s || !y_perm) return MOE_ERR_ARG;
   if (!aligned16(h_q, w_down_q, y_perm)) return MOE_ERR_ARG;
-  return from_hip(launch_down_fp8((const uint8_t*)h_q, h_s, expert_offsets, max_rows, E, d, I,
+  return from_hip(launch_down_fp8((const uint8_t*)h_q, I, h_s, expert_offsets, max_rows, E, d, I,
                                   (const uint8_t*)w_down_q, w_down_s, (bf16_t*)y_perm, (hipStream_t)stream));
 }
 
@@ -185,10 +194,13 @@ moe_status moe_grouped_ffn_fp8(const void* x_q, const float* x_s, const int32_t*
   const Ffn8Layout L = ffn8_layout(max_rows, I);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   char* ws = (char*)workspace;
-  TRY(moe_gate_up_swiglu_fp8(x_q, x_s, expert_offsets, max_rows, E, d, I, w_gate_up_q, w_gate_up_s, nullptr, 0,
-                             ws + L.h_q, (float*)(ws + L.h_s), stream));
-  return moe_down_proj_fp8(ws + L.h_q, (const float*)(ws + L.h_s), expert_offsets, max_rows, E, d, I, w_down_q,
-                           w_down_s, y_perm, stream);
+  const int ldh = row_bytes8(max_rows, I);
+  hipStream_t s = (hipStream_t)stream;
+  TRY(from_hip(launch_gate_up_fp8((const uint8_t*)x_q, d, x_s, expert_offsets, max_rows, E, d, I,
+                                  (const uint8_t*)w_gate_up_q, w_gate_up_s, nullptr, 0, (uint8_t*)(ws + L.h_q), ldh,
+                                  (float*)(ws + L.h_s), s)));
+  return from_hip(launch_down_fp8((const uint8_t*)(ws + L.h_q), ldh, (const float*)(ws + L.h_s), expert_offsets,
+                                  max_rows, E, d, I, (const uint8_t*)w_down_q, w_down_s, (bf16_t*)y_perm, s));
 }
 
 size_t moe_forward_fp8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I) {
@@ -224,10 +236,11 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
   hipStream_t s = (hipStream_t)stream;
   if (logits) TRY(from_hip(launch_route_topk(logits, T, E, k, topk_idx, topk_w, s)));
   TRY(from_hip(launch_permute_index(topk_idx, P, k, E, r_tok, p_row, offs, ws + L.perm_ws, s)));
-  TRY(from_hip(launch_quantize_rows_bf16((const bf16_t*)x, T, d, x_q, x_s, s)));
-  TRY(from_hip(launch_gate_up_fp8(x_q, x_s, offs, P, E, d, I, (const uint8_t*)w_gate_up_q, w_gate_up_s, r_tok, T, h_q,
-                                  h_s, s)));
-  TRY(from_hip(launch_down_fp8(h_q, h_s, offs, P, E, d, I, (const uint8_t*)w_down_q, w_down_s, y, s)));
+  const int ldx = row_bytes8(T, d), ldh = row_bytes8(P, I);
+  TRY(from_hip(launch_quantize_rows_bf16((const bf16_t*)x, T, d, x_q, ldx, x_s, s)));
+  TRY(from_hip(launch_gate_up_fp8(x_q, ldx, x_s, offs, P, E, d, I, (const uint8_t*)w_gate_up_q, w_gate_up_s, r_tok, T,
+                                  h_q, ldh, h_s, s)));
+  TRY(from_hip(launch_down_fp8(h_q, ldh, h_s, offs, P, E, d, I, (const uint8_t*)w_down_q, w_down_s, y, s)));
   return from_hip(launch_combine_bf16(y, P, p_row, topk_w, T, k, d, (bf16_t*)out, s));
 }
 

@@ -311,10 +311,11 @@ hipError_t launch_wgrad_f32(const float* a, int lda, int M, const float* b, int 
 
 // ---- 8-bit codes and scales (quantize.hip) ----
 // rows and expert weights to e4m3 with a float32 scale for each block of 128
-// (layouts in include/moe_serving.h)
-hipError_t launch_quantize_rows_bf16(const bf16_t* x, int64_t rows, int cols, uint8_t* q, float* scale,
+// (layouts in include/moe_serving.h; rows of codes ldq bytes apart)
+hipError_t launch_quantize_rows_bf16(const bf16_t* x, int64_t rows, int cols, uint8_t* q, int ldq, float* scale,
                                      hipStream_t s);
-hipError_t launch_quantize_rows_f32(const float* x, int64_t rows, int cols, uint8_t* q, float* scale, hipStream_t s);
+hipError_t launch_quantize_rows_f32(const float* x, int64_t rows, int cols, uint8_t* q, int ldq, float* scale,
+                                    hipStream_t s);
 hipError_t launch_quantize_weights_bf16(const bf16_t* wgu, const bf16_t* wd, int E, int d, int I, uint8_t* gu_q,
                                         float* gu_s, uint8_t* dn_q, float* dn_s, hipStream_t s);
 hipError_t launch_quantize_weights_f32(const float* wgu, const float* wd, int E, int d, int I, uint8_t* gu_q,
@@ -322,12 +323,14 @@ hipError_t launch_quantize_weights_f32(const float* wgu, const float* wd, int E,
 
 // ---- grouped products in 8 bits (fp8_ffn.hip) ----
 // xq [x_rows or max_rows, d], wq [E, 2I, d] -> codes hq [max_rows, I] and
-// their scales; with row_token, row r is x's row row_token[r]
-hipError_t launch_gate_up_fp8(const uint8_t* xq, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
+// their scales; with row_token, row r is x's row row_token[r].  ldx, ldh: bytes
+// between rows of codes (multiples of 16; those of 128 let a stage's loads
+// take whole cache lines)
+hipError_t launch_gate_up_fp8(const uint8_t* xq, int ldx, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
                               int d, int I, const uint8_t* wq, const float* ws, const int32_t* row_token,
-                              int64_t x_rows, uint8_t* hq, float* hs, hipStream_t s);
+                              int64_t x_rows, uint8_t* hq, int ldh, float* hs, hipStream_t s);
 // hq [max_rows, I], wq [E, d, I] -> y [max_rows, d]
-hipError_t launch_down_fp8(const uint8_t* hq, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
+hipError_t launch_down_fp8(const uint8_t* hq, int ldh, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
                            int d, int I, const uint8_t* wq, const float* ws, bf16_t* y, hipStream_t s);
 
 // ---- the layer for a few tokens (few.hip) ----

@@ -39,7 +39,8 @@ constexpr int kGroupM = 8;                       // row tiles of a weight slice 
 constexpr uint32_t kPark = 0x80000000u;          // past every buffer: reads zeros
 
 struct Gemm8Args {
-  const uint8_t* a;          // rows [*, K]
+  const uint8_t* a;          // rows [*, K], lda bytes apart
+  int64_t lda;
   const float* a_s;          // [*, KB]
   const int32_t* row_token;  // gathered rows, or null
   int64_t a_rows;            // rows of a
@@ -48,7 +49,8 @@ struct Gemm8Args {
   int E, K, N;               // N: output columns (gate/up: I)
   const uint8_t* w;          // [E, NW, K], NW = 2 N for gate/up
   const float* w_s;
-  void* out;                 // gate/up: codes [max_rows, N]; down: bf16 [max_rows, N]
+  void* out;                 // gate/up: codes [max_rows, N], ldo bytes apart; down: bf16 [max_rows, N]
+  int64_t ldo;
   float* out_s;              // gate/up: [max_rows, NB]
 };
 
@@ -110,6 +112,13 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   __shared__ uint32_t s_amax[GATE_UP ? WN * BM : 1];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n_tiles = (g.N + TN - 1) / TN;
+#ifdef MOE_DEVICE_CHECKS
+  // (here and not where a row is used: a trap inside the tile loop would make
+  // its uniform values differ between lanes)
+  if (blockIdx.x == 0 && g.row_token)
+    for (int64_t r = tid; r < clampi<int64_t>(g.offsets[g.E], 0, g.max_rows); r += kThreads8)
+      MOE_DCHECK(g.row_token[r] >= 0 && g.row_token[r] < g.a_rows);
+#endif
 
   // ---- the experts' row tiles, counted from the offsets
   {
@@ -177,7 +186,6 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
       int64_t src = -1;
       if (tid < t.rows) {
         src = g.row_token[t.row0 + tid];
-        MOE_DCHECK(src >= 0 && src < g.a_rows);
         src = src >= 0 && src < g.a_rows ? src : -1;
       }
       s_rows[tid] = (int)src;
@@ -191,8 +199,8 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   auto aim = [&](const Tile8& t) {
     const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
     const int64_t a_span = gather ? g.a_rows : t.rows;
-    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * K), (short)0,
-                                               (int)(a_span * K), kBufferConfig);
+    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * g.lda), (short)0,
+                                               (int)(a_span * g.lda), kBufferConfig);
     as_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a_s : g.a_s + t.row0 * KB), (short)0,
                                                 (int)(a_span * KB * 4), kBufferConfig);
     w_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w + t.e * w_rows * K), (short)0, (int)(w_rows * K),
@@ -204,7 +212,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
     for (int p = 0; p < A_PER; ++p) {
       const int i = wave + NW * p;
       const int r = i < A_LOADS ? source_row(8 * i + ln / 8) : -1;
-      a_off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)K + piece;
+      a_off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)g.lda + piece;
     }
 #pragma unroll
     for (int p = 0; p < B_PER; ++p) {
@@ -371,7 +379,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         bool finite;
         power_scale(a, scale, inv, finite);
         if (wn == 0 && eq == 0) g.out_s[(t.row0 + r) * NB + t.n0 / 128] = scale;
-        uint8_t* o = (uint8_t*)g.out + (t.row0 + r) * g.N;
+        uint8_t* o = (uint8_t*)g.out + (t.row0 + r) * g.ldo;
 #pragma unroll
         for (int f = 0; f < NF / 2; ++f) {
           const int col = t.n0 + wn * (BW / 2) + f * 16 + eq * 4;
@@ -425,15 +433,15 @@ hipError_t gemm8_any(const Gemm8Args& g, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_gate_up_fp8(const uint8_t* xq, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
+hipError_t launch_gate_up_fp8(const uint8_t* xq, int ldx, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
                               int d, int I, const uint8_t* wq, const float* ws, const int32_t* row_token,
-                              int64_t x_rows, uint8_t* hq, float* hs, hipStream_t s) {
-  return gemm8_any<true>({xq, xs, row_token, x_rows, expert_offsets, max_rows, E, d, I, wq, ws, hq, hs}, s);
+                              int64_t x_rows, uint8_t* hq, int ldh, float* hs, hipStream_t s) {
+  return gemm8_any<true>({xq, ldx, xs, row_token, x_rows, expert_offsets, max_rows, E, d, I, wq, ws, hq, ldh, hs}, s);
 }
 
-hipError_t launch_down_fp8(const uint8_t* hq, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
+hipError_t launch_down_fp8(const uint8_t* hq, int ldh, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
                            int d, int I, const uint8_t* wq, const float* ws, bf16_t* y, hipStream_t s) {
-  return gemm8_any<false>({hq, hs, nullptr, max_rows, expert_offsets, max_rows, E, I, d, wq, ws, y, nullptr}, s);
+  return gemm8_any<false>({hq, ldh, hs, nullptr, max_rows, expert_offsets, max_rows, E, I, d, wq, ws, y, 0, nullptr}, s);
 }
 
 }  // namespace tre

@@ -43,18 +43,19 @@ constexpr int kRowThreads = 256, kRowUnroll = 4;
 
 template <typename Elem>
 __global__ __launch_bounds__(kRowThreads) void k_quantize_rows(const Elem* __restrict__ x, uint32_t n_blocks, int cols,
-                                                               int nb, uint8_t* __restrict__ q,
+                                                               int nb, uint8_t* __restrict__ q, int ldq,
                                                                float* __restrict__ scale) {
   const int l16 = threadIdx.x % 16;
   const uint32_t first = blockIdx.x * (kRowThreads / 16 * kRowUnroll) + threadIdx.x / 16;
   float f[kRowUnroll][8];
-  int64_t at[kRowUnroll];
+  int64_t at[kRowUnroll], to[kRowUnroll];
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u) {
     const uint32_t b = first + u * (kRowThreads / 16);
     const uint32_t row = b / (uint32_t)nb;
     const int c = (int)(b - row * nb) * kBlock + l16 * 8;
     at[u] = b < n_blocks && c < cols ? (int64_t)row * cols + c : -1;   // the last block may be half a block
+    to[u] = (int64_t)row * ldq + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
     if (at[u] >= 0) load8(x + at[u], f[u]);
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(kRowThreads) void k_quantize_rows(const Elem* __res
       float* v = f[u];
       const uint32_t lo = pack_fp8x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
       const uint32_t hi = pack_fp8x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-      *(uint2*)(q + at[u]) = finite ? make_uint2(lo, hi) : make_uint2(kNan8, kNan8);
+      *(uint2*)(q + to[u]) = finite ? make_uint2(lo, hi) : make_uint2(kNan8, kNan8);
     }
   }
 }
@@ -150,11 +151,11 @@ __global__ __launch_bounds__(256) void k_quantize_weights(const Elem* __restrict
 }
 
 template <typename Elem>
-hipError_t rows(const Elem* x, int64_t n, int cols, uint8_t* q, float* scale, hipStream_t s) {
+hipError_t rows(const Elem* x, int64_t n, int cols, uint8_t* q, int ldq, float* scale, hipStream_t s) {
   const int nb = (int)ceil_div(cols, kBlock);
   const int64_t blocks = n * nb;
   k_quantize_rows<Elem><<<(unsigned)ceil_div(blocks, kRowThreads / 16 * kRowUnroll), kRowThreads, 0, s>>>(
-      x, (uint32_t)blocks, cols, nb, q, scale);
+      x, (uint32_t)blocks, cols, nb, q, ldq, scale);
   return hipGetLastError();
 }
 
@@ -169,11 +170,13 @@ hipError_t weights(const Elem* wgu, const Elem* wd, int E, int d, int I, uint8_t
 
 }  // namespace
 
-hipError_t launch_quantize_rows_bf16(const bf16_t* x, int64_t n, int cols, uint8_t* q, float* scale, hipStream_t s) {
-  return rows(x, n, cols, q, scale, s);
+hipError_t launch_quantize_rows_bf16(const bf16_t* x, int64_t n, int cols, uint8_t* q, int ldq, float* scale,
+                                     hipStream_t s) {
+  return rows(x, n, cols, q, ldq, scale, s);
 }
-hipError_t launch_quantize_rows_f32(const float* x, int64_t n, int cols, uint8_t* q, float* scale, hipStream_t s) {
-  return rows(x, n, cols, q, scale, s);
+hipError_t launch_quantize_rows_f32(const float* x, int64_t n, int cols, uint8_t* q, int ldq, float* scale,
+                                    hipStream_t s) {
+  return rows(x, n, cols, q, ldq, scale, s);
 }
 hipError_t launch_quantize_weights_bf16(const bf16_t* wgu, const bf16_t* wd, int E, int d, int I, uint8_t* gu_q,
                                         float* gu_s, uint8_t* dn_q, float* dn_s, hipStream_t s) {
