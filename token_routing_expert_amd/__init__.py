@@ -114,9 +114,15 @@ def load(build_if_missing: bool = True):
 
 # ---- marshalling helpers ----------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t) -> int:
@@ -517,28 +523,35 @@ FEW_MAX_PAIRS = 1024
 
 
 class _Call:
-    """Where one call runs: the device of its first tensor and its stream."""
+    """Where one call runs: the device of its first tensor and its stream.  (Written for the few microseconds that
+    a decode step's launches take: no objects and no lookups that a call does not need.)"""
+
+    __slots__ = ("torch", "device", "given", "raw")
 
     def __init__(self, like, stream):
-        torch = _torch()
+        torch = self.torch = _torch()
         if not like.is_cuda:
             raise ValueError("tensors passed to the MoE library must live on the GPU")
-        self.device = like.device
-        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
-        if self.stream.device != self.device:
-            raise ValueError(f"stream of {self.stream.device}, tensors on {self.device}")
-        self.given = stream is not None
+        self.device = device = like.device
+        self.given = stream
+        if stream is None:
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device}, tensors on {device}")
+            self.raw = stream.cuda_stream
 
     def empty(self, shape, dtype):
-        torch = _torch()
-        if not self.given:
+        """A new tensor that belongs to the call's stream."""
+        torch = self.torch
+        if self.given is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
+        with torch.cuda.stream(self.given):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def tensor(self, t, dtype, shape, name):
         """t's address, after its type, shape, device and layout are checked."""
-        if t.dtype != dtype or t.shape != shape:
+        if t.dtype is not dtype or t.shape != shape:
             raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
         if t.device != self.device:
             raise ValueError(f"{name}: on {t.device}, expected {self.device}")
@@ -547,24 +560,24 @@ class _Call:
         return t.data_ptr()
 
     def workspace(self, t, nbytes):
-        torch = _torch()
+        """(the workspace, its address): t if it is large enough, or a new one."""
         if t is None:
-            return self.empty((max(nbytes, 1),), torch.uint8)
-        if t.device != self.device or not t.is_contiguous():
+            t = self.empty((max(nbytes, 1),), self.torch.uint8)
+        elif t.device != self.device or not t.is_contiguous():
             raise ValueError(f"workspace: a contiguous tensor on {self.device} is needed")
-        if t.numel() * t.element_size() < nbytes:
+        elif t.numel() * t.element_size() < nbytes:
             raise ValueError(f"workspace holds {t.numel() * t.element_size()} bytes, {nbytes} needed")
-        return t
+        return t, t.data_ptr()
 
     def run(self, name, fn, *args):
         """The C call, with the device current (the library launches on the current device)."""
-        torch = _torch()
-        if torch.cuda.current_device() == self.device.index:
-            status = fn(*args, self.stream.cuda_stream)
+        torch = self.torch
+        if torch._C._cuda_getDevice() == self.device.index:
+            status = fn(*args, self.raw)
         else:
             with torch.cuda.device(self.device):
-                status = fn(*args, self.stream.cuda_stream)
-        if status != 0:
+                status = fn(*args, self.raw)
+        if status:
             raise MoeError(name, status)
 
 
@@ -700,9 +713,9 @@ def moe_grouped_ffn_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, w_do
     po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
     y_perm = c.empty((R, d), torch.bfloat16) if y_perm is None else y_perm
     nbytes = lib.moe_grouped_ffn_fp8_workspace_size(R, I)
-    ws = c.workspace(workspace, nbytes)
+    ws, pwork = c.workspace(workspace, nbytes)
     c.run("moe_grouped_ffn_fp8", lib.moe_grouped_ffn_fp8, px, ps, po, R, E, d, I, *pws,
-          c.tensor(y_perm, torch.bfloat16, (R, d), "y_perm"), ws.data_ptr(), nbytes)
+          c.tensor(y_perm, torch.bfloat16, (R, d), "y_perm"), pwork, nbytes)
     return y_perm
 
 
@@ -726,9 +739,9 @@ def moe_forward_fp8(x, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, k: int, log
           for name, t, n in (("expert_offsets", expert_offsets, E + 1), ("row_token", row_token, T * k),
                              ("pair_row", pair_row, T * k))]
     nbytes = lib.moe_forward_fp8_workspace_size(T, d, E, k, I)
-    ws = c.workspace(workspace, nbytes)
+    ws, pwork = c.workspace(workspace, nbytes)
     c.run("moe_forward_fp8", lib.moe_forward_fp8, px, plg, T, d, E, k, I, *pws, pi, pw, *ix,
-          c.tensor(out, torch.bfloat16, (T, d), "out"), ws.data_ptr(), nbytes)
+          c.tensor(out, torch.bfloat16, (T, d), "out"), pwork, nbytes)
     return out, topk_idx, topk_w
 
 
@@ -754,9 +767,9 @@ def moe_forward_few(x, w_gate_up, w_down, k: int, logits=None, topk_idx=None, to
     plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
     out = c.empty((T, d), x.dtype) if out is None else out
     nbytes = lib.moe_forward_few_workspace_size(T, d, E, k, I, dt)
-    ws = c.workspace(workspace, nbytes)
+    ws, pwork = c.workspace(workspace, nbytes)
     c.run("moe_forward_few", lib.moe_forward_few, px, plg, T, d, E, k, I, pgu, pd, dt, pi, pw,
-          c.tensor(out, x.dtype, (T, d), "out"), ws.data_ptr(), nbytes)
+          c.tensor(out, x.dtype, (T, d), "out"), pwork, nbytes)
     return out, topk_idx, topk_w
 
 
@@ -777,7 +790,7 @@ def moe_forward_few_fp8(x, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, k: int,
     plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
     out = c.empty((T, d), torch.bfloat16) if out is None else out
     nbytes = lib.moe_forward_few_fp8_workspace_size(T, d, E, k, I)
-    ws = c.workspace(workspace, nbytes)
+    ws, pwork = c.workspace(workspace, nbytes)
     c.run("moe_forward_few_fp8", lib.moe_forward_few_fp8, px, plg, T, d, E, k, I, *pws, pi, pw,
-          c.tensor(out, torch.bfloat16, (T, d), "out"), ws.data_ptr(), nbytes)
+          c.tensor(out, torch.bfloat16, (T, d), "out"), pwork, nbytes)
     return out, topk_idx, topk_w
