@@ -9,10 +9,10 @@
 // beside each matrix instruction of 32 cycles, in the shadow of the other
 // waves' matrix work.
 //
-// Tile: BM rows x 256 weight rows, one block of 128 bytes of k a stage, both
+// Tile: BM rows x BN weight rows, one block of 128 bytes of k a stage, both
 // operands loaded straight to LDS (16-byte chunk c of row r in slot
 // c ^ (r & 7), so that consecutive rows of one chunk fall into different
-// banks), two stages: the next one loads while this one multiplies.  Weights
+// banks), a ring of NS stages: NS - 1 load while one multiplies.  Weights
 // are the instruction's first operand, so a lane ends up with four consecutive
 // columns of one row and needs one row scale a fragment.  The row's scales and
 // the tile's weight scales ride along in the stage.
@@ -33,7 +33,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads8 = 512, kBN = 256, kStageK = 128;
+constexpr int kThreads8 = 512, kStageK = 128;
 constexpr int kCus = 256, kXcds = 8;             // workgroups are dealt round-robin over the XCDs
 constexpr int kGroupM = 8;                       // row tiles of a weight slice that run together
 constexpr uint32_t kPark = 0x80000000u;          // past every buffer: reads zeros
@@ -63,10 +63,10 @@ __device__ __forceinline__ void dma4s(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds_
                : "memory");
 }
 
-template <int BM>
+template <int BM, int BN>
 struct Stage8 {
   uint8_t a[BM * kStageK];
-  uint8_t b[kBN * kStageK];
+  uint8_t b[BN * kStageK];
   float as[(BM + 63) / 64 * 64];   // whole loads of 64
   float bs[64];              // [0], [1]: the tile's two weight blocks
 };
@@ -98,13 +98,18 @@ struct Tile8 {
   int64_t row0;
 };
 
-template <bool GATE_UP, int BM, int WM>
+template <bool GATE_UP, int BM, int BN, int WM, int NS>
 __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
-  constexpr int NW = kThreads8 / kWave, WN = NW / WM, MF = BM / 16 / WM, NF = kBN / 16 / WN, BW = kBN / WN;
-  constexpr int TN = GATE_UP ? kBN / 2 : kBN;      // output columns of a tile
-  constexpr int A_LOADS = BM / 8, B_LOADS = kBN / 8;   // 1 KB loads of a stage
-  constexpr int A_PER = (A_LOADS + NW - 1) / NW, B_PER = B_LOADS / NW;
-  __shared__ __attribute__((aligned(1024))) Stage8<BM> st[2];
+  constexpr int NW = kThreads8 / kWave, WN = NW / WM, MF = BM / 16 / WM, NF = BN / 16 / WN, BW = BN / WN;
+  constexpr int TN = GATE_UP ? BN / 2 : BN;      // output columns of a tile
+  // a stage's 1 KB loads, dealt to the waves: rows first, then weights; every
+  // wave issues PER of them and one of scales (of zeros into the sink where
+  // there is none), so that all count the same
+  constexpr int A_LOADS = BM / 8, LOADS = A_LOADS + BN / 8, PER = (LOADS + NW - 1) / NW, COUNT = PER + 1;
+  constexpr int AS_WAVES = (BM + 63) / 64;
+  static_assert(AS_WAVES < NW && (NS - 2) * COUNT < 64, "scale loads and the load counter");
+  __shared__ __attribute__((aligned(1024))) Stage8<BM, BN> st[NS];
+  __shared__ uint8_t s_sink[1024];
   __shared__ int s_tiles[kMaxExperts];    // row tiles of the experts up to and with this one
   __shared__ int s_wave[4];
   __shared__ int s_found[2][3];           // expert, row tile, column tile
@@ -193,60 +198,60 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   };
 
   // ---- the operands of the tile whose stages are being loaded
-  __amdgpu_buffer_rsrc_t a_rsrc, as_rsrc, w_rsrc, ws_rsrc;
-  uint32_t a_off[A_PER], b_off[B_PER], as_off = kPark, bs_off = kPark;
-  constexpr int AS_WAVES = (BM + 63) / 64;
+  __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc, s_rsrc;   // s: this wave's scales
+  uint32_t off[PER], s_off;
   auto aim = [&](const Tile8& t) {
     const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
     const int64_t a_span = gather ? g.a_rows : t.rows;
     a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * g.lda), (short)0,
                                                (int)(a_span * g.lda), kBufferConfig);
-    as_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a_s : g.a_s + t.row0 * KB), (short)0,
-                                                (int)(a_span * KB * 4), kBufferConfig);
     w_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w + t.e * w_rows * K), (short)0, (int)(w_rows * K),
                                                kBufferConfig);
-    ws_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w_s + t.e * ws_rows * KB), (short)0,
-                                                (int)(ws_rows * KB * 4), kBufferConfig);
     auto source_row = [&](int r) { return r >= t.rows ? -1 : gather ? s_rows[r] : r; };
 #pragma unroll
-    for (int p = 0; p < A_PER; ++p) {
+    for (int p = 0; p < PER; ++p) {
       const int i = wave + NW * p;
-      const int r = i < A_LOADS ? source_row(8 * i + ln / 8) : -1;
-      a_off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)g.lda + piece;
-    }
-#pragma unroll
-    for (int p = 0; p < B_PER; ++p) {
-      const int r = 8 * (wave + NW * p) + ln / 8;
-      int64_t src;
-      if constexpr (GATE_UP) {
-        const int col = t.n0 + r / BW * (BW / 2) + r % (BW / 2);
-        src = col < g.N ? (int64_t)(r % BW / (BW / 2)) * g.N + col : -1;
+      if (i < A_LOADS) {
+        const int r = source_row(8 * i + ln / 8);
+        off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)g.lda + piece;
       } else {
-        src = t.n0 + r < g.N ? t.n0 + r : -1;
+        const int r = 8 * (i - A_LOADS) + ln / 8;
+        int64_t src = -1;
+        if constexpr (GATE_UP) {
+          const int col = t.n0 + r / BW * (BW / 2) + r % (BW / 2);
+          if (i < LOADS && col < g.N) src = (int64_t)(r % BW / (BW / 2)) * g.N + col;
+        } else {
+          if (i < LOADS && t.n0 + r < g.N) src = t.n0 + r;
+        }
+        off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
       }
-      b_off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
     }
-    if (wave < AS_WAVES) {
-      const int r = wave * 64 + ln < BM ? source_row(wave * 64 + ln) : -1;
-      as_off = r < 0 ? kPark : (uint32_t)r * (uint32_t)(KB * 4);
-    }
-    if (wave == NW - 1 && ln < 2) {
-      const int64_t b = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
-      bs_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
-    }
+    const bool rows = wave < AS_WAVES;
+    const float* scales = !rows ? g.w_s + t.e * ws_rows * KB : gather ? g.a_s : g.a_s + t.row0 * KB;
+    const int64_t span = rows ? a_span : ws_rows;
+    s_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(scales), (short)0,
+                                               __builtin_amdgcn_readfirstlane((int)(span * KB * 4)), kBufferConfig);
+    int64_t at = -1;
+    if (rows && wave * 64 + ln < BM) at = source_row(wave * 64 + ln);
+    if (wave == NW - 1 && ln < 2) at = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
+    s_off = at >= 0 && at < span ? (uint32_t)at * (uint32_t)(KB * 4) : kPark;
   };
-  auto issue = [&](int step, int buf) {
-    Stage8<BM>* s = &st[buf];
+  auto issue = [&](int step, int slot) {
+    Stage8<BM, BN>* s = &st[slot];
     const bool cut = tail && step == steps - 1 && chunk >= 4;
 #pragma unroll
-    for (int p = 0; p < B_PER; ++p)
-      dma16s(w_rsrc, lds_address(s->b) + (wave + NW * p) * 1024, cut ? kPark : b_off[p], step * kStageK);
-#pragma unroll
-    for (int p = 0; p < A_PER; ++p)
-      if (A_LOADS % NW == 0 || wave + NW * p < A_LOADS)
-        dma16s(a_rsrc, lds_address(s->a) + (wave + NW * p) * 1024, cut ? kPark : a_off[p], step * kStageK);
-    if (wave < AS_WAVES) dma4s(as_rsrc, lds_address(s->as) + wave * 256, as_off, step * 4);
-    if (wave == NW - 1) dma4s(ws_rsrc, lds_address(s->bs), bs_off, step * 4);
+    for (int p = 0; p < PER; ++p) {
+      const int i = wave + NW * p;
+      if (i < A_LOADS)
+        dma16s(a_rsrc, lds_address(s->a) + i * 1024, cut ? kPark : off[p], step * kStageK);
+      else
+        dma16s(w_rsrc, i < LOADS ? lds_address(s->b) + (i - A_LOADS) * 1024 : lds_address(s_sink),
+               cut ? kPark : off[p], step * kStageK);
+    }
+    const uint32_t to = wave < AS_WAVES  ? lds_address(s->as) + wave * 256
+                        : wave == NW - 1 ? lds_address(s->bs)
+                                         : lds_address(s_sink);
+    dma4s(s_rsrc, to, s_off, step * 4);
   };
 
   // ---- the products
@@ -254,7 +259,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   const int place = l16 * kStageK + ((q ^ (l16 & 7)) * 16);   // rows are 16 apart: l16 & 7 is row & 7
   f32x4 acc[MF][NF];
   // the weights' fragments stay in registers, the rows' go by
-  auto multiply = [&](auto count, const Stage8<BM>& s) {
+  auto multiply = [&](auto count, const Stage8<BM, BN>& s) {
     constexpr int M = decltype(count)::value;
     const float s0 = GATE_UP ? s.bs[0] : s.bs[wn * BW / 128], s1 = GATE_UP ? s.bs[1] : 0.f;
     const uint8_t *a_lo = s.a + wm * 16 * kStageK + place, *a_hi = s.a + wm * 16 * kStageK + (place ^ 64);
@@ -298,8 +303,13 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   fetch_rows(t);
   __syncthreads();
   aim(t);
-  issue(0, 0);
-  int buf = 0, which = 0;
+  int in_flight = 0, to = 0, from = 0, which = 0;   // stages issued and not multiplied; next slots to fill and to read
+  auto fill = [&](int step) {
+    issue(step, to);
+    to = to + 1 == NS ? 0 : to + 1;
+    ++in_flight;
+  };
+  for (int s = 0; s < NS - 1 && s < steps; ++s) fill(s);
   while (true) {
     const int frags = (t.rows + 15) / 16;
     const int live = frags > wm ? (frags - wm + WM - 1) / WM : 0;   // this wave's fragments that hold rows
@@ -310,28 +320,37 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 #pragma unroll
       for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto walk = [&](auto count) {
+      int filled = 0;   // stages of the next tile on their way, once it is aimed at
+      bool aimed = false;
+      auto look = [&]() {   // the next tile's place
+        find(tile + stride, which ^ 1);
+        lds_barrier();
+        next = found(which ^ 1);
+        fetch_rows(next);
+      };
       for (int step = 0; step < steps; ++step) {
-        // this wave's loads of the stage have landed and its reads of the
-        // other buffer have returned (vmcnt and lgkmcnt 0); with the barrier,
-        // everyone's
-        __builtin_amdgcn_s_waitcnt(7 << 4);
+        // this wave's loads of the stage have landed (all but the younger
+        // stages'; near the end all) and its reads of the last one have
+        // returned; with the barrier, everyone's, and that slot is free
+        if (NS > 2 && in_flight >= NS - 1) wait_vmcnt<(NS - 2) * COUNT>(); else wait_vmcnt<0>();
+        __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));   // lgkmcnt(0)
         stage_barrier();
-        if (step + 1 < steps) issue(step + 1, buf ^ 1);
-        // the next tile's place is found behind the first stage's barrier, and
-        // its first stage loads while this tile's last one multiplies
-        if (step == 0 && more) {
-          find(tile + stride, which ^ 1);
+        if (step == 0 && more && steps < NS) {
+          look();
           lds_barrier();
-          next = found(which ^ 1);
-          fetch_rows(next);
         }
-        if (step + 1 == steps && more) {
-          if (steps == 1) lds_barrier();
-          aim(next);
-          issue(0, buf ^ 1);
+        // the stage NS - 1 ahead: this tile's, or behind its last one the next tile's
+        if (step + NS - 1 < steps) {
+          fill(step + NS - 1);
+        } else if (more) {
+          if (!aimed) aim(next);
+          aimed = true;
+          while (filled < steps && in_flight < NS) fill(filled++);
         }
-        if constexpr (decltype(count)::value > 0) multiply(count, st[buf]);
-        buf ^= 1;
+        if (step == 0 && more && steps >= NS) look();
+        if constexpr (decltype(count)::value > 0) multiply(count, st[from]);
+        from = from + 1 == NS ? 0 : from + 1;
+        --in_flight;
       }
     };
     // as many fragments as hold rows, in steps of two (one without rows is
@@ -355,7 +374,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
           for (int f = 0; f < NF / 2; ++f)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              const float gate = acc[m][f][v], h = gate / (1.f + expf(-gate)) * acc[m][f + NF / 2][v];
+              const float h = swiglu(acc[m][f][v], acc[m][f + NF / 2][v]);
               acc[m][f][v] = h;
               top[m] = abs_bits(h) > top[m] ? abs_bits(h) : top[m];
             }
@@ -409,26 +428,54 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   }
 }
 
-template <bool GATE_UP, int BM, int WM>
+// Tile height by the mean number of rows an expert gets: the lowest of 32, 64,
+// 128 and 288 that holds one and a half times as many, so that most experts
+// take one tile and their weights are loaded once (32768 rows, 128 experts, 2880
+// x 2880: 288-row tiles 507 us, 256-row ones 561) -- but no higher than gives
+// every compute unit a tile (2048 rows, 4 experts, 1024 x 704: gate/up 33 us in
+// 48 tiles of 288 rows, 17 in 384 of 32; down 27 and, in 256 of 64, 10.5).
+// columns: output columns of a tile of each height.
+int tile_rows(const Gemm8Args& g, const int (&columns)[4]) {
+  const int heights[4] = {32, 64, 128, 288};
+  const int64_t mean = ceil_div(g.max_rows, g.E);
+  int h = 0;
+  while (h < 3 && heights[h] < mean + mean / 2) ++h;
+  while (h > 0 && g.E * ceil_div(mean, heights[h]) * ceil_div(g.N, columns[h]) < kCus) --h;
+  return heights[h];
+}
+
+template <bool GATE_UP, int BM, int BN, int WM, int NS>
 hipError_t gemm8(const Gemm8Args& g, hipStream_t s) {
   // every expert may leave one partly filled tile
   const int64_t m_tiles = g.max_rows / BM + (g.max_rows < g.E ? g.max_rows : g.E);
-  const int64_t tiles = m_tiles * ceil_div(g.N, GATE_UP ? kBN / 2 : kBN);
-  const int64_t most = kCus * (2 * sizeof(Stage8<BM>) * 2 < 150 * 1024 ? 2 : 1);   // resident workgroups, by LDS
-  k_gemm8<GATE_UP, BM, WM><<<(unsigned)(tiles < most ? round_up(tiles, kXcds) : most), kThreads8, 0, s>>>(g);
+  const int64_t tiles = m_tiles * ceil_div(g.N, GATE_UP ? BN / 2 : BN);
+  // resident workgroups: by LDS (2 KB beside the stages, and what gate/up exchanges), at most 4 by their waves
+  constexpr int fit = 160 * 1024 / (int)(NS * sizeof(Stage8<BM, BN>) + 4096 + (GATE_UP ? 8 / WM * BM * 4 : 0) + BM * 4);
+  const int64_t most = kCus * (fit > 4 ? 4 : fit);
+  k_gemm8<GATE_UP, BM, BN, WM, NS><<<(unsigned)(tiles < most ? round_up(tiles, kXcds) : most), kThreads8, 0, s>>>(g);
   return hipGetLastError();
 }
 
-// Tile height by the mean number of rows an expert gets: the lowest that holds
-// one and a half times as many, so that most experts take one tile and their
-// weights are loaded once.
-template <bool GATE_UP>
-hipError_t gemm8_any(const Gemm8Args& g, hipStream_t s) {
-  const int64_t mean = ceil_div(g.max_rows, g.E), want = mean + mean / 2;
-  if (want <= 32) return gemm8<GATE_UP, 32, 1>(g, s);
-  if (want <= 64) return gemm8<GATE_UP, 64, 1>(g, s);
-  if (want <= 128) return gemm8<GATE_UP, 128, 2>(g, s);
-  return gemm8<GATE_UP, 288, 2>(g, s);
+hipError_t gate_up8(const Gemm8Args& g, hipStream_t s) {
+  switch (tile_rows(g, {128, 128, 128, 128})) {
+    case 32: return gemm8<true, 32, 256, 1, 2>(g, s);
+    case 64: return gemm8<true, 64, 256, 1, 3>(g, s);
+    case 128: return gemm8<true, 128, 256, 2, 3>(g, s);
+    default: return gemm8<true, 288, 256, 2, 2>(g, s);
+  }
+}
+
+// Lower tiles are narrower: with few rows the weights' stream is the work, and
+// more, smaller workgroups keep more of it in flight (64 rows, 16 experts, 8192 x
+// 5120: 32 rows by 64 columns and three stages 121 us, by 256 and two 143; 8192
+// rows, 16 experts, 2816 x 1024: 128 x 128 39 us, 128 x 256 41, 288 x 256 62).
+hipError_t down8(const Gemm8Args& g, hipStream_t s) {
+  switch (tile_rows(g, {64, 128, 128, 256})) {
+    case 32: return gemm8<false, 32, 64, 2, 3>(g, s);
+    case 64: return gemm8<false, 64, 128, 1, 2>(g, s);
+    case 128: return gemm8<false, 128, 128, 2, 2>(g, s);
+    default: return gemm8<false, 288, 256, 2, 2>(g, s);
+  }
 }
 
 }  // namespace
@@ -436,12 +483,12 @@ hipError_t gemm8_any(const Gemm8Args& g, hipStream_t s) {
 hipError_t launch_gate_up_fp8(const uint8_t* xq, int ldx, const float* xs, const int32_t* expert_offsets, int64_t max_rows, int E,
                               int d, int I, const uint8_t* wq, const float* ws, const int32_t* row_token,
                               int64_t x_rows, uint8_t* hq, int ldh, float* hs, hipStream_t s) {
-  return gemm8_any<true>({xq, ldx, xs, row_token, x_rows, expert_offsets, max_rows, E, d, I, wq, ws, hq, ldh, hs}, s);
+  return gate_up8({xq, ldx, xs, row_token, x_rows, expert_offsets, max_rows, E, d, I, wq, ws, hq, ldh, hs}, s);
 }
 
 hipError_t launch_down_fp8(const uint8_t* hq, int ldh, const float* hs, const int32_t* expert_offsets, int64_t max_rows, int E,
                            int d, int I, const uint8_t* wq, const float* ws, bf16_t* y, hipStream_t s) {
-  return gemm8_any<false>({hq, ldh, hs, nullptr, max_rows, expert_offsets, max_rows, E, I, d, wq, ws, y, 0, nullptr}, s);
+  return down8({hq, ldh, hs, nullptr, max_rows, expert_offsets, max_rows, E, I, d, wq, ws, y, 0, nullptr}, s);
 }
 
 }  // namespace tre
