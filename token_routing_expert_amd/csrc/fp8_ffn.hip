@@ -102,14 +102,16 @@ template <bool GATE_UP, int BM, int BN, int WM, int NS>
 __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   constexpr int NW = kThreads8 / kWave, WN = NW / WM, MF = BM / 16 / WM, NF = BN / 16 / WN, BW = BN / WN;
   constexpr int TN = GATE_UP ? BN / 2 : BN;      // output columns of a tile
-  // a stage's 1 KB loads, dealt to the waves: rows first, then weights; every
-  // wave issues PER of them and one of scales (of zeros into the sink where
-  // there is none), so that all count the same
-  constexpr int A_LOADS = BM / 8, LOADS = A_LOADS + BN / 8, PER = (LOADS + NW - 1) / NW, COUNT = PER + 1;
+  // a stage's 1 KB loads, dealt to the waves: weights first (they come from
+  // further away), then rows, then one of scales.  With more than two stages
+  // the waits count loads, so every wave issues as many: of zeros into the
+  // sink where it has none.
+  constexpr int A_LOADS = BM / 8, B_PER = BN / 8 / NW, A_PER = (A_LOADS + NW - 1) / NW, COUNT = B_PER + A_PER + 1;
   constexpr int AS_WAVES = (BM + 63) / 64;
-  static_assert(AS_WAVES < NW && (NS - 2) * COUNT < 64, "scale loads and the load counter");
+  constexpr bool EVEN = NS > 2;
+  static_assert(BN % (8 * NW) == 0 && AS_WAVES < NW && (NS - 2) * COUNT < 64, "loads, scale loads, the load counter");
   __shared__ __attribute__((aligned(1024))) Stage8<BM, BN> st[NS];
-  __shared__ uint8_t s_sink[1024];
+  __shared__ uint8_t s_sink[NS > 2 ? 1024 : 4];
   __shared__ int s_tiles[kMaxExperts];    // row tiles of the experts up to and with this one
   __shared__ int s_wave[4];
   __shared__ int s_found[2][3];           // expert, row tile, column tile
@@ -197,9 +199,10 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
     }
   };
 
-  // ---- the operands of the tile whose stages are being loaded
-  __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc, s_rsrc;   // s: this wave's scales
-  uint32_t off[PER], s_off;
+  // ---- the operands of the tile whose stages are being loaded (a descriptor
+  // each: one chosen by wave for the scales made the loop 4% slower)
+  __amdgpu_buffer_rsrc_t a_rsrc, as_rsrc, w_rsrc, ws_rsrc;
+  uint32_t a_off[A_PER], b_off[B_PER], as_off = kPark, bs_off = kPark;
   auto aim = [&](const Tile8& t) {
     const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
     const int64_t a_span = gather ? g.a_rows : t.rows;
@@ -209,49 +212,51 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
                                                kBufferConfig);
     auto source_row = [&](int r) { return r >= t.rows ? -1 : gather ? s_rows[r] : r; };
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int i = wave + NW * p;
-      if (i < A_LOADS) {
-        const int r = source_row(8 * i + ln / 8);
-        off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)g.lda + piece;
+    for (int p = 0; p < B_PER; ++p) {
+      const int r = 8 * (wave + NW * p) + ln / 8;
+      int64_t src = -1;
+      if constexpr (GATE_UP) {
+        const int col = t.n0 + r / BW * (BW / 2) + r % (BW / 2);
+        if (col < g.N) src = (int64_t)(r % BW / (BW / 2)) * g.N + col;
       } else {
-        const int r = 8 * (i - A_LOADS) + ln / 8;
-        int64_t src = -1;
-        if constexpr (GATE_UP) {
-          const int col = t.n0 + r / BW * (BW / 2) + r % (BW / 2);
-          if (i < LOADS && col < g.N) src = (int64_t)(r % BW / (BW / 2)) * g.N + col;
-        } else {
-          if (i < LOADS && t.n0 + r < g.N) src = t.n0 + r;
-        }
-        off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
+        if (t.n0 + r < g.N) src = t.n0 + r;
       }
+      b_off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
     }
-    const bool rows = wave < AS_WAVES;
-    const float* scales = !rows ? g.w_s + t.e * ws_rows * KB : gather ? g.a_s : g.a_s + t.row0 * KB;
-    const int64_t span = rows ? a_span : ws_rows;
-    s_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(scales), (short)0,
-                                               __builtin_amdgcn_readfirstlane((int)(span * KB * 4)), kBufferConfig);
-    int64_t at = -1;
-    if (rows && wave * 64 + ln < BM) at = source_row(wave * 64 + ln);
-    if (wave == NW - 1 && ln < 2) at = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
-    s_off = at >= 0 && at < span ? (uint32_t)at * (uint32_t)(KB * 4) : kPark;
+#pragma unroll
+    for (int p = 0; p < A_PER; ++p) {
+      const int i = wave + NW * p, r = i < A_LOADS ? source_row(8 * i + ln / 8) : -1;
+      a_off[p] = r < 0 ? kPark : (uint32_t)r * (uint32_t)g.lda + piece;
+    }
+    as_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a_s : g.a_s + t.row0 * KB), (short)0,
+                                                (int)(a_span * KB * 4), kBufferConfig);
+    ws_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w_s + t.e * ws_rows * KB), (short)0,
+                                                (int)(ws_rows * KB * 4), kBufferConfig);
+    if (wave < AS_WAVES) {
+      const int r = wave * 64 + ln < BM ? source_row(wave * 64 + ln) : -1;
+      as_off = r < 0 ? kPark : (uint32_t)r * (uint32_t)(KB * 4);
+    }
+    if (wave == NW - 1 && ln < 2) {
+      const int64_t b = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
+      bs_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
+    }
   };
   auto issue = [&](int step, int slot) {
     Stage8<BM, BN>* s = &st[slot];
     const bool cut = tail && step == steps - 1 && chunk >= 4;
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
+    for (int p = 0; p < B_PER; ++p)
+      dma16s(w_rsrc, lds_address(s->b) + (wave + NW * p) * 1024, cut ? kPark : b_off[p], step * kStageK);
+#pragma unroll
+    for (int p = 0; p < A_PER; ++p) {
       const int i = wave + NW * p;
-      if (i < A_LOADS)
-        dma16s(a_rsrc, lds_address(s->a) + i * 1024, cut ? kPark : off[p], step * kStageK);
-      else
-        dma16s(w_rsrc, i < LOADS ? lds_address(s->b) + (i - A_LOADS) * 1024 : lds_address(s_sink),
-               cut ? kPark : off[p], step * kStageK);
+      if (EVEN || A_LOADS % NW == 0 || i < A_LOADS)
+        dma16s(a_rsrc, !EVEN || i < A_LOADS ? lds_address(s->a) + i * 1024 : lds_address(s_sink),
+               cut ? kPark : a_off[p], step * kStageK);
     }
-    const uint32_t to = wave < AS_WAVES  ? lds_address(s->as) + wave * 256
-                        : wave == NW - 1 ? lds_address(s->bs)
-                                         : lds_address(s_sink);
-    dma4s(s_rsrc, to, s_off, step * 4);
+    if (wave < AS_WAVES) dma4s(as_rsrc, lds_address(s->as) + wave * 256, as_off, step * 4);
+    else if (wave == NW - 1) dma4s(ws_rsrc, lds_address(s->bs), bs_off, step * 4);
+    else if (EVEN) dma4s(ws_rsrc, lds_address(s_sink), kPark, step * 4);
   };
 
   // ---- the products
@@ -309,7 +314,11 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
     to = to + 1 == NS ? 0 : to + 1;
     ++in_flight;
   };
-  for (int s = 0; s < NS - 1 && s < steps; ++s) fill(s);
+  if constexpr (NS == 2) {
+    issue(0, 0);
+  } else {
+    for (int s = 0; s < NS - 1 && s < steps; ++s) fill(s);
+  }
   while (true) {
     const int frags = (t.rows + 15) / 16;
     const int live = frags > wm ? (frags - wm + WM - 1) / WM : 0;   // this wave's fragments that hold rows
@@ -328,6 +337,27 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         next = found(which ^ 1);
         fetch_rows(next);
       };
+      if constexpr (NS == 2) {
+        // two stages: one loads while the other multiplies.  (The ring below
+        // does the same with NS = 2, 5% slower: it has two places to issue from.)
+        for (int step = 0; step < steps; ++step) {
+          // this wave's loads of the stage have landed and its reads of the
+          // other slot have returned (vmcnt and lgkmcnt 0); with the barrier,
+          // everyone's
+          __builtin_amdgcn_s_waitcnt(7 << 4);
+          stage_barrier();
+          if (step + 1 < steps) issue(step + 1, from ^ 1);
+          if (step == 0 && more) look();
+          if (step + 1 == steps && more) {
+            if (steps == 1) lds_barrier();
+            aim(next);
+            issue(0, from ^ 1);
+          }
+          if constexpr (decltype(count)::value > 0) multiply(count, st[from]);
+          from ^= 1;
+        }
+        return;
+      }
       for (int step = 0; step < steps; ++step) {
         // this wave's loads of the stage have landed (all but the younger
         // stages'; near the end all) and its reads of the last one have
