@@ -8,7 +8,7 @@
  *
  * Inference only: none of these has a backward pass.  Rows, weights, outputs
  * and workspaces of these calls begin at multiples of 16 bytes (MOE_ERR_ARG
- * otherwise).
+ * otherwise); d and I are below 2^22, beside moe.h's limits.
  *
  * The 8-bit format.  A code is e4m3 (OCP: sign, 4 bits of exponent with bias
  * 7, 3 of mantissa; largest 448, no infinities, 0x7F and 0xFF are NaN).  A

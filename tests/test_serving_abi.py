@@ -153,6 +153,23 @@ def test_few(lib, fp8):
         assert lib.moe_forward_few_workspace_size(*sizes.values(), 3) == 0
 
 
+def test_widths_below_2_22(lib):
+    """A tile's rows of codes are addressed with 31 bits: wider layers are refused by every call that takes one."""
+    big = 1 << 22
+    assert lib.moe_quantize_weights(FAKE, FAKE, 1, 1, big, 64, FAKE, FAKE, FAKE, FAKE, None) == UNSUPPORTED
+    assert lib.moe_down_proj_fp8(FAKE, FAKE, FAKE, 4, 1, 64, big, FAKE, FAKE, FAKE, None) == UNSUPPORTED
+    assert lib.moe_gate_up_swiglu_fp8(FAKE, FAKE, FAKE, 4, 1, big, 64, FAKE, FAKE, None, 0, FAKE, FAKE,
+                                      None) == UNSUPPORTED
+    assert lib.moe_grouped_ffn_fp8(FAKE, FAKE, FAKE, 4, 1, 64, big, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40,
+                                   None) == UNSUPPORTED
+    assert lib.moe_forward_fp8(FAKE, FAKE, 1, big, 1, 1, 64, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, FAKE,
+                               FAKE, 1 << 40, None) == UNSUPPORTED
+    assert lib.moe_forward_few(FAKE, FAKE, 1, 64, 1, 1, big, FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, 1 << 40,
+                               None) == UNSUPPORTED
+    assert lib.moe_forward_few_fp8(FAKE, FAKE, 1, big, 1, 1, 64, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                   1 << 40, None) == UNSUPPORTED
+
+
 def test_binding_refuses(lib):
     """What the binding itself checks, with host tensors: nothing reaches the library."""
     import torch

@@ -642,6 +642,76 @@ def test_few_two_streams(tre, form):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
 
 
+def test_layer8_two_streams(tre):
+    """The 8-bit layer on two streams at once, each call's workspace its own."""
+    torch = T()
+    T_, d, E, k, I = 300, 320, 8, 2, 256
+    w, _, _ = weights8(E, d, I, 150)
+    xs = [rand((T_, d), "bf16", 151 + i)[0] for i in range(2)]
+    lgs = [routed(T_, E, k, 153 + i)[0] for i in range(2)]
+    want = [tre.moe_forward_fp8(x, *w, k, logits=lg) for x, lg in zip(xs, lgs)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sync()
+    got = [tre.moe_forward_fp8(xs[i % 2], *w, k, logits=lgs[i % 2], stream=streams[i % 2]) for i in range(10)]
+    sync()
+    for i, o in enumerate(got):
+        for a, b in zip(o, want[i % 2]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+
+
+def test_two_graphs_share_a_workspace(tre):
+    """Two captured steps of different sizes in one workspace, replayed in turn: each finds the other's leftovers."""
+    torch = T()
+    d, E, k, I = 192, 8, 2, 128
+    w, _, _ = few_weights("bf16", E, d, I, 160)
+    ws = torch.full((max(tre.moe_forward_few_workspace_size(t, d, E, k, I, tre.MOE_BF16) for t in (3, 40)),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    runs = []
+    for t in (3, 40):
+        x, lg = rand((t, d), "bf16", 161 + t)[0], routed(t, E, k, 162 + t)[0]
+        want = tre.moe_forward_few(x, *w, k, logits=lg)[0]
+        out = torch.empty_like(x)
+        idx, wt = torch.empty((t, k), dtype=torch.int32, device="cuda"), torch.empty((t, k), device="cuda")
+        call = lambda x=x, lg=lg, out=out, idx=idx, wt=wt: tre.moe_forward_few(   # noqa: E731
+            x, *w, k, logits=lg, topk_idx=idx, topk_w=wt, out=out, workspace=ws)
+        runs.append((captured(torch, call), out, want, call))   # call holds the tensors that the graph reads
+    for r in range(6):
+        g, out, want, _ = runs[r % 2]
+        out.fill_(float("nan"))
+        g.replay()
+        sync()
+        assert torch.equal(out, want), r
+
+
+@pytest.mark.parametrize("T_,d,E,k,I", [(1, 128, 4, 2, 64), (40, 192, 16, 3, 320), (700, 256, 4, 2, 576)])
+def test_device_checked_build_equals_release(tre, T_, d, E, k, I):
+    """libmoe_debug.so (valid input only: a value outside its contract stops it) gives the same bits."""
+    import os
+    torch = T()
+    assert os.path.exists(tre.DEBUG_LIB_PATH), "libmoe_debug.so is not built"
+    dbg = tre.open_library(tre.DEBUG_LIB_PATH)
+    w, _, _ = weights8(E, d, I, 170)
+    wb, _, _ = few_weights("bf16", E, d, I, 171)
+    x, _ = rand((T_, d), "bf16", 172)
+    lg, _ = routed(T_, E, k, 173)
+    calls = [lambda: tre.moe_quantize_rows(x), lambda: tre.moe_quantize_weights(*wb),
+             lambda: tre.moe_forward_fp8(x, *w, k, logits=lg)]
+    if T_ <= 64:
+        calls += [lambda: tre.moe_forward_few(x, *wb, k, logits=lg),
+                  lambda: tre.moe_forward_few_fp8(x, *w, k, logits=lg)]
+    release = tre.load()
+    for call in calls:
+        a = call()
+        try:
+            tre._lib = dbg
+            b = call()
+        finally:
+            tre._lib = release
+        sync()
+        for u, v in zip(a, b):
+            assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+
+
 def test_binding_checks(tre):
     torch = T()
     x, _ = rand((4, 128), "bf16", 1)

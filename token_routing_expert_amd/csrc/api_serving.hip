@@ -17,11 +17,15 @@ bool aligned16(const P*... p) {
   return ((((uintptr_t)p & 15) == 0) && ...);
 }
 
+// A row tile of 288 rows of 8-bit codes is addressed with 31 bits.
+constexpr int32_t kMaxWidth = 1 << 22;
+
 // E experts of widths d and I.
 moe_status check_layer(int32_t E, int32_t d, int32_t I) {
   TRY(check_experts(E));
   TRY(check_width(d));
   TRY(check_width(I));
+  if (d >= kMaxWidth || I >= kMaxWidth) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)E * d * 2 * I >= 8 * kMaxElems) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)d * I * 4 >= kMaxElems) return MOE_ERR_UNSUPPORTED;   // one expert's bf16 gate/up weights < 2 GiB
   return MOE_OK;

@@ -505,6 +505,7 @@ __global__ __launch_bounds__(M::kDnWaves * kWave, 2) void k_few_down(
           }
         }
       });
+      compiler_fence();
       wait_vmcnt<0>();
       __syncthreads();
       if (tid == 0)
