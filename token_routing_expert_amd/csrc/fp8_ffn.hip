@@ -417,37 +417,66 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         }
       }
       lds_barrier();   // (not a full one: the next tile's stage is on its way)
+      // the codes gather in the slot that was multiplied last, 128 bytes a row
+      // (16-byte chunk c in place c ^ (row & 7)), and leave as whole lines
+      uint8_t* rows_out = st[from == 0 ? NS - 1 : from - 1].a;
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
         const int r = (m * WM + wm) * 16 + er;
-        if (m >= live || r >= t.rows) continue;
+        if (m >= live) continue;
         uint32_t a = 0;
 #pragma unroll
         for (int w = 0; w < WN; ++w) a = s_amax[w * BM + r] > a ? s_amax[w * BM + r] : a;
         float scale, inv;
         bool finite;
         power_scale(a, scale, inv, finite);
-        if (wn == 0 && eq == 0) g.out_s[(t.row0 + r) * NB + t.n0 / 128] = scale;
-        uint8_t* o = (uint8_t*)g.out + (t.row0 + r) * g.ldo;
+        if (wn == 0 && eq == 0 && r < t.rows) g.out_s[(t.row0 + r) * NB + t.n0 / 128] = scale;
 #pragma unroll
         for (int f = 0; f < NF / 2; ++f) {
-          const int col = t.n0 + wn * (BW / 2) + f * 16 + eq * 4;
-          const uint32_t c = pack_fp8x4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv, acc[m][f][3] * inv);
-          if (col < g.N) *(uint32_t*)(o + col) = finite ? c : kNan8;
+          const int c = wn * (BW / 32) + f;
+          const uint32_t v = pack_fp8x4(acc[m][f][0] * inv, acc[m][f][1] * inv, acc[m][f][2] * inv, acc[m][f][3] * inv);
+          *(uint32_t*)(rows_out + r * 128 + ((c ^ (r & 7)) * 16) + eq * 4) = finite ? v : kNan8;
         }
       }
+      lds_barrier();
+      const int et = fresh(tid);
+#pragma unroll
+      for (int i = 0; i < BM * 8; i += kThreads8) {
+        const int r = (i + et) / 8, c = et % 8;
+        if (r < t.rows && t.n0 + c * 16 < g.N)
+          *(u32x4*)((uint8_t*)g.out + (t.row0 + r) * g.ldo + t.n0 + c * 16) =
+              *(const u32x4*)(rows_out + r * 128 + ((c ^ (r & 7)) * 16));
+      }
     } else {
+      // rows gather in the slot that was multiplied last, as many at a time as
+      // it holds (16-byte chunk c in place c ^ (row & 7)), and leave as whole
+      // lines
+      constexpr int ROW = BN * 2, PASS_M = (BM + BN) * kStageK / (ROW * WM * 16) < MF ? 4 : MF, PASS = PASS_M * WM * 16;
+      static_assert(PASS * ROW <= (BM + BN) * kStageK, "a pass fits a stage");
+      uint8_t* rows_out = st[from == 0 ? NS - 1 : from - 1].a;
+      const int et = fresh(tid);
 #pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        const int r = (m * WM + wm) * 16 + er;
-        if (m >= live || r >= t.rows) continue;
-        bf16_t* o = (bf16_t*)g.out + (t.row0 + r) * g.N;
+      for (int m0 = 0; m0 < MF; m0 += PASS_M) {
+        if (m0 * WM * 16 >= t.rows) break;
+        lds_barrier();   // the stage's, or the last pass's, readers are done
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const int col = t.n0 + wn * BW + f * 16 + eq * 4;
-          if (col < g.N)
-            *(uint2*)(o + col) = make_uint2(pack_bf16x2(acc[m][f][0], acc[m][f][1]),
-                                            pack_bf16x2(acc[m][f][2], acc[m][f][3]));
+        for (int m = m0; m < m0 + PASS_M && m < MF; ++m) {
+          const int r = ((m - m0) * WM + wm) * 16 + er;
+          if (m >= live) continue;
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            const int c = wn * (BW / 8) + f * 2 + eq / 2;
+            *(uint2*)(rows_out + r * ROW + ((c ^ (r & 7)) * 16) + eq % 2 * 8) = make_uint2(
+                pack_bf16x2(acc[m][f][0], acc[m][f][1]), pack_bf16x2(acc[m][f][2], acc[m][f][3]));
+          }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < PASS * (ROW / 16); i += kThreads8) {
+          const int r = (i + et) / (ROW / 16), c = (i + et) % (ROW / 16), at = m0 * WM * 16 + r;
+          if (r < PASS && at < t.rows && t.n0 + c * 8 < g.N)
+            *(u32x4*)((bf16_t*)g.out + (t.row0 + at) * g.N + t.n0 + c * 8) =
+                *(const u32x4*)(rows_out + r * ROW + ((c ^ (r & 7)) * 16));
         }
       }
     }
