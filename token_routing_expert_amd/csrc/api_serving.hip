@@ -67,7 +67,7 @@ size_t scale_bytes(int64_t rows, int64_t cols) { return (size_t)(rows * ceil_div
 // Bytes between rows of 8-bit codes in a workspace: whole cache lines, where
 // that keeps the array's offsets below 2^31 (the caller's own arrays are
 // dense; 2880 columns are 22.5 lines, and every other row's loads then take
-// two halves for each line: the 128-expert layer's products are 8% slower).
+// two halves for each line: the 128-expert layer's products are 4% slower).
 int row_bytes8(int64_t rows, int64_t cols) {
   const int64_t padded = round_up(cols, 128);
   return (int)(rows * padded < kMaxElems ? padded : cols);
