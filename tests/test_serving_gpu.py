@@ -299,6 +299,52 @@ def test_products_exact(tre, counts, d, I):
         at += n
 
 
+def spread_groups(rows):
+    """24 experts of about `rows` rows: enough tiles for every height, with an empty expert, one row, one row past a
+    tile's edge, and one expert of several tiles."""
+    counts = np.random.default_rng(rows).integers(rows // 2, rows + rows // 2, 24)
+    counts[[0, 5, 7, 9]] = 0, 1, rows * 2 + 1, rows * 5
+    return [int(c) for c in counts]
+
+
+@pytest.mark.parametrize("rows", [30, 60, 96, 144])                # tiles of 64, 128 and 288 rows
+@pytest.mark.parametrize("K", [64, 192, 320, 384, 512, 1088])      # 1 to 9 stages, with and without half a block
+def test_products_exact_many_tiles(tre, rows, K):
+    """As above with more tiles than compute units, so that a workgroup walks from one tile to the next; the exact
+    sums in 64 bits on the GPU."""
+    torch = T()
+    counts, I, N = spread_groups(rows), 1408, 2880
+    R, E, kb = sum(counts), len(counts), ref.blocks(K)
+    offs = offsets_of(counts)
+
+    def spread(codes, scales):   # [n, k] codes with scales [n / 128 or n, k / 128]
+        s = scales.double().repeat_interleave(128, 1)[:, :codes.shape[1]]
+        s = s if s.shape[0] == codes.shape[0] else s.repeat_interleave(128, 0)[:codes.shape[0]]
+        return codes.float().double() * s
+
+    xq, xs = short_codes((R, K), 5), power_scales((R, kb), 6)
+    wq, ws = short_codes((E, N, K), 3), power_scales((E, ref.blocks(N), kb), 4)
+    y = tre.moe_down_proj_fp8(xq, xs, offs, wq, ws)
+    at = 0
+    for e, n in enumerate(counts):
+        exact = spread(xq[at:at + n], xs[at:at + n]) @ spread(wq[e], ws[e]).t().contiguous()
+        assert torch.equal(y[at:at + n], exact.float().to(torch.bfloat16)), (e, n)
+        at += n
+    gq, gs = short_codes((E, 2 * I, K), 1), power_scales((E, 2, ref.blocks(I), kb), 2)
+    xs *= 0.125
+    token = to_device(np.random.default_rng(K).permutation(R).astype(np.int32))
+    hq, hs = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, gq, gs, row_token=token)
+    at = 0
+    for e, n in enumerate(counts):
+        if n:
+            r = token[at:at + n].long()
+            x = spread(xq.view(torch.uint8)[r].view(torch.float8_e4m3fn), xs[r])
+            gu = torch.cat([x @ spread(gq[e, i * I:(i + 1) * I], gs[e, i]).t().contiguous() for i in (0, 1)], 1)
+            h, eh = ref.swiglu(gu.cpu().numpy(), np.zeros((n, 2 * I)))
+            check_codes(hq[at:at + n], hs[at:at + n], h, eh, f"expert {e} of {counts}")
+        at += n
+
+
 def test_gate_up_rows_out_of_range(tre):
     """A row_token outside [0, x_rows) reads zeros: its h is zero, and no other row changes."""
     torch = T()

@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   // sink where it has none.
   constexpr int A_LOADS = BM / 8, B_PER = BN / 8 / NW, A_PER = (A_LOADS + NW - 1) / NW, COUNT = B_PER + A_PER + 1;
   constexpr int AS_WAVES = (BM + 63) / 64;
-  constexpr bool EVEN = NS > 2;
+  constexpr bool EVEN = NS > 2, AHEAD = BM > 128;   // AHEAD: two slots, weights two stages ahead (below)
   static_assert(BN % (8 * NW) == 0 && AS_WAVES < NW && (NS - 2) * COUNT < 64, "loads, scale loads, the load counter");
   __shared__ __attribute__((aligned(1024))) Stage8<BM, BN> st[NS];
   __shared__ uint8_t s_sink[NS > 2 ? 1024 : 4];
@@ -187,11 +187,12 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   // Finds a tile's expert and place; `which` alternates.  One thread writes,
   // everyone reads after the next barrier.
   auto find = [&](int64_t tile, int which) {
+    const int width = fresh(n_tiles);   // (the divisions' reciprocals stay out of the tile loop's registers)
     if (tid < kMaxExperts) {
-      const int64_t hi = (int64_t)s_tiles[tid] * n_tiles, lo = tid ? (int64_t)s_tiles[tid - 1] * n_tiles : 0;
+      const int64_t hi = (int64_t)s_tiles[tid] * width, lo = tid ? (int64_t)s_tiles[tid - 1] * width : 0;
       if (tile >= lo && tile < hi) {
-        const int m_tiles = (int)((hi - lo) / n_tiles), at = (int)(tile - lo);
-        const int group = at / (kGroupM * n_tiles), in = at - group * (kGroupM * n_tiles);
+        const int m_tiles = (int)((hi - lo) / width), at = (int)(tile - lo);
+        const int group = at / (kGroupM * width), in = at - group * (kGroupM * width);
         const int wide = m_tiles - group * kGroupM < kGroupM ? m_tiles - group * kGroupM : kGroupM;
         s_found[which][0] = tid;
         s_found[which][1] = group * kGroupM + in % wide;
@@ -223,15 +224,11 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   // ---- the operands of the tile whose stages are being loaded (a descriptor
   // each: one chosen by wave for the scales made the loop 4% slower)
   __amdgpu_buffer_rsrc_t a_rsrc, as_rsrc, w_rsrc, ws_rsrc;
-  uint32_t a_off[A_PER], b_off[B_PER], as_off = kPark, bs_off = kPark;
-  auto aim = [&](const Tile8& t) {
+  uint32_t a_off[A_PER], b_off[B_PER], scale_off = kPark;
+  auto aim_weights = [&](const Tile8& t) {
     const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
-    const int64_t a_span = gather ? g.a_rows : t.rows;
-    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * g.lda), (short)0,
-                                               (int)(a_span * g.lda), kBufferConfig);
     w_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(g.w + t.e * w_rows * K), (short)0, (int)(w_rows * K),
                                                kBufferConfig);
-    auto source_row = [&](int r) { return r >= t.rows ? -1 : gather ? s_rows[r] : r; };
 #pragma unroll
     for (int p = 0; p < B_PER; ++p) {
       const int r = 8 * (wave + NW * p) + ln / 8;
@@ -244,6 +241,13 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
       }
       b_off[p] = src < 0 ? kPark : (uint32_t)(src * K + piece);
     }
+  };
+  auto aim_rows = [&](const Tile8& t) {
+    const int ln = fresh(lane), piece = ((ln & 7) ^ (ln >> 3)) * 16;
+    const int64_t a_span = gather ? g.a_rows : t.rows;
+    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(uniform_ptr(gather ? g.a : g.a + t.row0 * g.lda), (short)0,
+                                               (int)(a_span * g.lda), kBufferConfig);
+    auto source_row = [&](int r) { return r >= t.rows ? -1 : gather ? s_rows[r] : r; };
 #pragma unroll
     for (int p = 0; p < A_PER; ++p) {
       const int i = wave + NW * p, r = i < A_LOADS ? source_row(8 * i + ln / 8) : -1;
@@ -255,19 +259,27 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
                                                 (int)(ws_rows * KB * 4), kBufferConfig);
     if (wave < AS_WAVES) {
       const int r = wave * 64 + ln < BM ? source_row(wave * 64 + ln) : -1;
-      as_off = r < 0 ? kPark : (uint32_t)r * (uint32_t)(KB * 4);
+      scale_off = r < 0 ? kPark : (uint32_t)r * (uint32_t)(KB * 4);
     }
     if (wave == NW - 1 && ln < 2) {
       const int64_t b = GATE_UP ? (int64_t)ln * NB + t.n0 / 128 : t.n0 / 128 + ln;
-      bs_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
+      scale_off = b < ws_rows ? (uint32_t)(b * KB * 4) : kPark;
     }
   };
-  auto issue = [&](int step, int slot) {
+  auto aim = [&](const Tile8& t) {
+    aim_weights(t);
+    aim_rows(t);
+  };
+  auto issue_weights = [&](int step, int slot) {
     Stage8<BM, BN>* s = &st[slot];
     const bool cut = tail && step == steps - 1 && chunk >= 4;
 #pragma unroll
     for (int p = 0; p < B_PER; ++p)
       dma16s(w_rsrc, lds_address(s->b) + (wave + NW * p) * 1024, cut ? kPark : b_off[p], step * kStageK);
+  };
+  auto issue_rows = [&](int step, int slot) {   // and both operands' scales
+    Stage8<BM, BN>* s = &st[slot];
+    const bool cut = tail && step == steps - 1 && chunk >= 4;
 #pragma unroll
     for (int p = 0; p < A_PER; ++p) {
       const int i = wave + NW * p;
@@ -275,9 +287,13 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         dma16s(a_rsrc, !EVEN || i < A_LOADS ? lds_address(s->a) + i * 1024 : lds_address(s_sink),
                cut ? kPark : a_off[p], step * kStageK);
     }
-    if (wave < AS_WAVES) dma4s(as_rsrc, lds_address(s->as) + wave * 256, as_off, step * 4);
-    else if (wave == NW - 1) dma4s(ws_rsrc, lds_address(s->bs), bs_off, step * 4);
+    if (wave < AS_WAVES) dma4s(as_rsrc, lds_address(s->as) + wave * 256, scale_off, step * 4);
+    else if (wave == NW - 1) dma4s(ws_rsrc, lds_address(s->bs), scale_off, step * 4);
     else if (EVEN) dma4s(ws_rsrc, lds_address(s_sink), kPark, step * 4);
+  };
+  auto issue = [&](int step, int slot) {
+    issue_weights(step, slot);
+    issue_rows(step, slot);
   };
 
   // ---- the products
@@ -285,7 +301,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   const int place = l16 * kStageK + ((q ^ (l16 & 7)) * 16);   // rows are 16 apart: l16 & 7 is row & 7
   f32x4 acc[MF][NF];
   // the weights' fragments stay in registers, the rows' go by
-  auto multiply = [&](auto count, const Stage8<BM, BN>& s) {
+  auto multiply = [&](auto count, const Stage8<BM, BN>& s, auto weights_read) {
     constexpr int M = decltype(count)::value;
     const float s0 = GATE_UP ? s.bs[0] : s.bs[wn * BW / 128], s1 = GATE_UP ? s.bs[1] : 0.f;
     const uint8_t *a_lo = s.a + wm * 16 * kStageK + place, *a_hi = s.a + wm * 16 * kStageK + (place ^ 64);
@@ -346,6 +362,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[m][f][v] = fmaf(c, part[f][v], acc[m][f][v]);
       }
+      if (m == 0) weights_read();
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -365,6 +382,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   };
   if constexpr (NS == 2) {
     issue(0, 0);
+    if constexpr (AHEAD) issue_weights(1, 1);
   } else {
     for (int s = 0; s < NS - 1 && s < steps; ++s) fill(s);
   }
@@ -387,22 +405,45 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         fetch_rows(next);
       };
       if constexpr (NS == 2) {
-        // two stages: one loads while the other multiplies.  (The ring below
-        // does the same with NS = 2, 2% slower: it has two places to issue from.)
+        // Two slots: one stage loads while the other multiplies.  (The ring
+        // below does the same with NS = 2, 2% slower: it has two places to
+        // issue from.)  AHEAD: a wave reads its weights at a stage's start and
+        // keeps them, so behind the first row fragment, once every wave has,
+        // the slot's half that held them takes those of the stage after the
+        // next (behind a tile's end the next tile's; the launch sees to it
+        // that a tile has three stages or more).  32768 rows, 128 experts, 2880
+        // x 2880: gate/up 831 -> 750 us, down 412 -> 394; 16 experts 762 -> 689
+        // and 338 -> 336.  Lower tiles gain nothing (64 rows: 50 and 52 us).
+        const int n_ahead = AHEAD ? steps - (more ? 1 : 2) : -1;   // stages that issue weights
         for (int step = 0; step < steps; ++step) {
-          // this wave's loads of the stage have landed and its reads of the
-          // other slot have returned (vmcnt and lgkmcnt 0); with the barrier,
-          // everyone's
-          __builtin_amdgcn_s_waitcnt(7 << 4);
+          // this wave's loads of the stage have landed -- with AHEAD all but
+          // its youngest, the next stage's weights -- and its reads of the
+          // other slot have returned (lgkmcnt 0); with the barrier, everyone's
+          if (step <= n_ahead) wait_vmcnt<AHEAD ? B_PER : 0>(); else wait_vmcnt<0>();
+          __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));   // lgkmcnt(0)
           stage_barrier();
-          if (step + 1 < steps) issue(step + 1, from ^ 1);
-          if (step == 0 && more) look();
-          if (step + 1 == steps && more) {
-            if (steps == 1) lds_barrier();
-            aim(next);
-            issue(0, from ^ 1);
+          if (step + 1 < steps) {
+            if constexpr (!AHEAD) issue_weights(step + 1, from ^ 1);
+            issue_rows(step + 1, from ^ 1);
           }
-          if constexpr (decltype(count)::value > 0) multiply(count, st[from]);
+          if (step == 0 && more) look();
+          if (AHEAD && step + 2 == steps && more) aim_weights(next);
+          if (step + 1 == steps && more) {
+            if constexpr (!AHEAD) {
+              if (steps == 1) lds_barrier();
+              aim_weights(next);
+              issue_weights(0, from ^ 1);
+            }
+            aim_rows(next);
+            issue_rows(0, from ^ 1);
+          }
+          auto weights_read = [&]() {
+            if (!AHEAD || step >= n_ahead) return;
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();   // this wave's reads have returned; with the barrier, everyone's
+            issue_weights(step + 2 < steps ? step + 2 : 0, from);
+          };
+          if constexpr (decltype(count)::value > 0) multiply(count, st[from], weights_read); else weights_read();
           from ^= 1;
         }
         return;
@@ -427,7 +468,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
           while (filled < steps && in_flight < NS) fill(filled++);
         }
         if (step == 0 && more && steps >= NS) look();
-        if constexpr (decltype(count)::value > 0) multiply(count, st[from]);
+        if constexpr (decltype(count)::value > 0) multiply(count, st[from], [] {});
         from = from + 1 == NS ? 0 : from + 1;
         --in_flight;
       }
@@ -530,6 +571,10 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
       }
     }
     if (!more) return;
+    if constexpr (AHEAD) {
+      lds_barrier();   // the results' readers are done
+      issue_weights(1, from ^ 1);
+    }
     tile += stride;
     which ^= 1;
     t = next;
@@ -542,6 +587,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 // x 2880: 288-row tiles 507 us, 256-row ones 561) -- but no higher than gives
 // every compute unit a tile (2048 rows, 4 experts, 1024 x 704: gate/up 33 us in
 // 48 tiles of 288 rows, 17 in 384 of 32; down 27 and, in 256 of 64, 10.5).
+// 288 rows need three stages of k (AHEAD).
 // columns: output columns of a tile of each height.
 int tile_rows(const Gemm8Args& g, const int (&columns)[4]) {
   const int heights[4] = {32, 64, 128, 288};
@@ -549,6 +595,7 @@ int tile_rows(const Gemm8Args& g, const int (&columns)[4]) {
   int h = 0;
   while (h < 3 && heights[h] < mean + mean / 2) ++h;
   while (h > 0 && g.E * ceil_div(mean, heights[h]) * ceil_div(g.N, columns[h]) < kCus) --h;
+  if (h == 3 && g.K <= 2 * kStageK) h = 2;
   return heights[h];
 }
 
