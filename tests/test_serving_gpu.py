@@ -307,13 +307,13 @@ def spread_groups(rows):
     return [int(c) for c in counts]
 
 
-@pytest.mark.parametrize("rows", [30, 60, 96, 144])                # tiles of 64, 128 and 288 rows
+@pytest.mark.parametrize("rows", [30, 60, 96, 144, 250])           # tiles of 64, 128 and 288 rows, 160 in the last
 @pytest.mark.parametrize("K", [64, 192, 320, 384, 512, 1088])      # 1 to 9 stages, with and without half a block
 def test_products_exact_many_tiles(tre, rows, K):
     """As above with more tiles than compute units, so that a workgroup walks from one tile to the next; the exact
     sums in 64 bits on the GPU."""
     torch = T()
-    counts, I, N = spread_groups(rows), 1408, 2880
+    counts, I, N = spread_groups(rows), 1408, 2880 if rows < 200 else 1408
     R, E, kb = sum(counts), len(counts), ref.blocks(K)
     offs = offsets_of(counts)
 

@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   // sink where it has none.
   constexpr int A_LOADS = BM / 8, B_PER = BN / 8 / NW, A_PER = (A_LOADS + NW - 1) / NW, COUNT = B_PER + A_PER + 1;
   constexpr int AS_WAVES = (BM + 63) / 64;
-  constexpr bool EVEN = NS > 2, AHEAD = BM > 128;   // AHEAD: two slots, weights two stages ahead (below)
+  constexpr bool EVEN = NS > 2, AHEAD = BM > 160;   // AHEAD: two slots, weights two stages ahead (below)
   static_assert(BN % (8 * NW) == 0 && AS_WAVES < NW && (NS - 2) * COUNT < 64, "loads, scale loads, the load counter");
   __shared__ __attribute__((aligned(1024))) Stage8<BM, BN> st[NS];
   __shared__ uint8_t s_sink[NS > 2 ? 1024 : 4];
@@ -620,6 +620,13 @@ hipError_t gate_up8(const Gemm8Args& g, hipStream_t s) {
   }
 }
 
+// The rows that the busiest compute unit walks through in tiles of h rows, with
+// every expert one standard deviation over the mean (random routing).
+int64_t longest_walk(const Gemm8Args& g, int h, int columns) {
+  const int64_t mean = ceil_div(g.max_rows, g.E), rows = mean + (int64_t)__builtin_sqrt((double)mean);
+  return h * ceil_div(g.E * ceil_div(rows, h) * ceil_div(g.N, columns), kCus);
+}
+
 // Lower tiles are narrower: with few rows the weights' stream is the work, and
 // more, smaller workgroups keep more of it in flight (64 rows, 16 experts, 8192 x
 // 5120: 32 rows by 64 columns and three stages 121 us, by 256 and two 143; 8192
@@ -628,7 +635,12 @@ hipError_t down8(const Gemm8Args& g, hipStream_t s) {
   switch (tile_rows(g, {64, 128, 128, 256})) {
     case 32: return gemm8<false, 32, 64, 2, 3>(g, s);
     case 64: return gemm8<false, 64, 128, 1, 2>(g, s);
-    case 128: return gemm8<false, 128, 128, 2, 2>(g, s);
+    case 128:
+      // 160 where the rows over a multiple of 128 would leave most units idle in
+      // the last round (8192 rows, 16 experts, 2816 x 1024: 34 us, 128 rows
+      // 43.5; 4096 rows 24 and 28; but 6144 rows 31.5 and 29, 10240 48 and 44)
+      if (longest_walk(g, 160, 128) < longest_walk(g, 128, 128)) return gemm8<false, 160, 128, 2, 2>(g, s);
+      return gemm8<false, 128, 128, 2, 2>(g, s);
     default: return gemm8<false, 288, 256, 2, 2>(g, s);
   }
 }
