@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
   // sink where it has none.
   constexpr int A_LOADS = BM / 8, B_PER = BN / 8 / NW, A_PER = (A_LOADS + NW - 1) / NW, COUNT = B_PER + A_PER + 1;
   constexpr int AS_WAVES = (BM + 63) / 64;
-  constexpr bool EVEN = NS > 2, AHEAD = BM > 160;   // AHEAD: two slots, weights two stages ahead (below)
+  constexpr bool EVEN = NS > 2, AHEAD = NS == 2 && BM >= 128 && BN == 256;   // AHEAD: weights two stages ahead (below)
   static_assert(BN % (8 * NW) == 0 && AS_WAVES < NW && (NS - 2) * COUNT < 64, "loads, scale loads, the load counter");
   __shared__ __attribute__((aligned(1024))) Stage8<BM, BN> st[NS];
   __shared__ uint8_t s_sink[NS > 2 ? 1024 : 4];
@@ -413,7 +413,10 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
         // next (behind a tile's end the next tile's; the launch sees to it
         // that a tile has three stages or more).  32768 rows, 128 experts, 2880
         // x 2880: gate/up 831 -> 750 us, down 412 -> 394; 16 experts 762 -> 689
-        // and 338 -> 336.  Lower tiles gain nothing (64 rows: 50 and 52 us).
+        // and 338 -> 336; gate/up in tiles of 128 rows, 1024 rows, 1024 x 2816,
+        // 31 -> 27 (there against three whole stages).  Lower tiles gain nothing
+        // (64 rows: 50 and 52 us) and narrower ones lose (8192 rows, 2816 x 1024
+        // in tiles of 160 x 128: 35 and 37).
         const int n_ahead = AHEAD ? steps - (more ? 1 : 2) : -1;   // stages that issue weights
         for (int step = 0; step < steps; ++step) {
           // this wave's loads of the stage have landed -- with AHEAD all but
@@ -587,15 +590,15 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 // x 2880: 288-row tiles 507 us, 256-row ones 561) -- but no higher than gives
 // every compute unit a tile (2048 rows, 4 experts, 1024 x 704: gate/up 33 us in
 // 48 tiles of 288 rows, 17 in 384 of 32; down 27 and, in 256 of 64, 10.5).
-// 288 rows need three stages of k (AHEAD).
-// columns: output columns of a tile of each height.
-int tile_rows(const Gemm8Args& g, const int (&columns)[4]) {
+// columns: output columns of a tile of each height; from height number `ahead`
+// on, tiles need three stages of k (AHEAD).
+int tile_rows(const Gemm8Args& g, const int (&columns)[4], int ahead) {
   const int heights[4] = {32, 64, 128, 288};
   const int64_t mean = ceil_div(g.max_rows, g.E);
   int h = 0;
   while (h < 3 && heights[h] < mean + mean / 2) ++h;
   while (h > 0 && g.E * ceil_div(mean, heights[h]) * ceil_div(g.N, columns[h]) < kCus) --h;
-  if (h == 3 && g.K <= 2 * kStageK) h = 2;
+  if (h >= ahead && g.K <= 2 * kStageK) h = ahead - 1;
   return heights[h];
 }
 
@@ -612,10 +615,10 @@ hipError_t gemm8(const Gemm8Args& g, hipStream_t s) {
 }
 
 hipError_t gate_up8(const Gemm8Args& g, hipStream_t s) {
-  switch (tile_rows(g, {128, 128, 128, 128})) {
+  switch (tile_rows(g, {128, 128, 128, 128}, 2)) {
     case 32: return gemm8<true, 32, 256, 1, 2>(g, s);
     case 64: return gemm8<true, 64, 256, 1, 3>(g, s);
-    case 128: return gemm8<true, 128, 256, 2, 3>(g, s);
+    case 128: return gemm8<true, 128, 256, 2, 2>(g, s);
     default: return gemm8<true, 288, 256, 2, 2>(g, s);
   }
 }
@@ -632,7 +635,7 @@ int64_t longest_walk(const Gemm8Args& g, int h, int columns) {
 // 5120: 32 rows by 64 columns and three stages 121 us, by 256 and two 143; 8192
 // rows, 16 experts, 2816 x 1024: 128 x 128 39 us, 128 x 256 41, 288 x 256 62).
 hipError_t down8(const Gemm8Args& g, hipStream_t s) {
-  switch (tile_rows(g, {64, 128, 128, 256})) {
+  switch (tile_rows(g, {64, 128, 128, 256}, 3)) {
     case 32: return gemm8<false, 32, 64, 2, 3>(g, s);
     case 64: return gemm8<false, 64, 128, 1, 2>(g, s);
     case 128:
