@@ -33,7 +33,14 @@
 //     48.5; 256 rows 52.0 and 49.7; 512 rows, 1024 x 2816, 31.9 and 26.7).  Higher
 //     ones are bound by the matrix work itself and stay in 8 bits (8192 tokens, 4
 //     of 128 experts, 2880 x 2880: 856 us, in bf16 1423; 1024 rows, 16 experts,
-//     1024 x 2816: 30.6 and 40.2), 0.22% to 0.45% off over forty shapes.
+//     1024 x 2816: 30.6 and 40.2; both before weights came two stages ahead),
+//     0.22% to 0.45% off over forty shapes.
+// Measured: down, 64 rows, 16 experts, 8192 x 5120: 124 us, 5.4 TB/s of weights;
+// 32768 rows, 16 experts, 2880 x 2880: 349 us, 1.56 PFLOP/s; gate/up of 32768
+// rows, 128 experts, 2880 x 2880: 806 us in the layer, 1.35 PFLOP/s.  With the
+// loads dropped the 32768-row product took 247 us, with the matrix instructions
+// dropped 296, loads alone 283: the three wait for each other at the stages'
+// barriers.
 // XCDs: consecutive tiles go to one XCD, in groups of up to 8 row tiles for
 // each weight slice, so that a slice is fetched once for the group and the
 // group's rows stay in that XCD's L2.
@@ -587,7 +594,7 @@ __global__ __launch_bounds__(kThreads8) void k_gemm8(Gemm8Args g) {
 // Tile height by the mean number of rows an expert gets: the lowest of 32, 64,
 // 128 and 288 that holds one and a half times as many, so that most experts
 // take one tile and their weights are loaded once (32768 rows, 128 experts, 2880
-// x 2880: 288-row tiles 507 us, 256-row ones 561) -- but no higher than gives
+// x 2880: 288-row tiles 507 us, 256-row ones 561, both before weights came ahead) -- but no higher than gives
 // every compute unit a tile (2048 rows, 4 experts, 1024 x 704: gate/up 33 us in
 // 48 tiles of 288 rows, 17 in 384 of 32; down 27 and, in 256 of 64, 10.5).
 // columns: output columns of a tile of each height; from height number `ahead`

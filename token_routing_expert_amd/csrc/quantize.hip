@@ -1,6 +1,9 @@
 // quantize.hip -- rows and expert weights to e4m3 codes with a float32 scale
 // for each block of 128 (activations: a row's 128 columns; weights: 128 x 128).
 // fp8.hpp has the arithmetic of a block.
+// One pass: a block's values stay in registers between its maximum and its codes.
+// Rows, measured: 8192 of 2880 bf16, 71.5 MB in 12.9 us, 5.5 TB/s (partly from the
+// caches); 4093 of 1024 float32 4.7 us; 64 of 5120 bf16 3.3 us, a launch's length.
 #include "fp8.hpp"
 
 namespace tre {
@@ -111,6 +114,8 @@ __global__ __launch_bounds__(kRowThreads) void k_quantize_rows(const Elem* __res
 // a code word of eight k for each n goes to LDS, and the block leaves as rows
 // of 128 bytes.  Blocks 0, 1, 2 of a triple are gate, up and down: all three
 // are ceil(I/128) x ceil(d/128) blocks, and one launch does the layer.
+// Bound by memory through lines of 128 bytes (a code row of a block): 16
+// experts, 1024 x 2816, bf16, 207 MB in 67 us, 3.1 TB/s.
 constexpr int kTileStride = kBlock + 4;    // bytes: 33 words, so that a wave's writes (8 rows apart) fill all banks
 
 template <typename Elem>
