@@ -101,7 +101,7 @@ def kernel(*lines):
     return "\n".join(["_Zk:"] + list(lines) + [".Lfunc_end0:"])
 
 
-def test_checker_sees_a_read_behind_a_branch():
+def test_a_read_behind_a_branch_is_seen():
     mfma = "v_mfma_f32_16x16x32_bf16 v[48:51], v[80:83], v[72:75], v[68:71]"
     seen, bad = early_readers(kernel(mfma, "s_cbranch_vccnz .LBB0_2", "s_nop 7", ".LBB0_2:", "v_fmac_f32_e32 v1, v2, v50"))
     assert seen == {"16x16x32": 1} and len(bad) == 1 and bad[0][3] == 1
