@@ -8,7 +8,10 @@
  *
  * Inference only: none of these has a backward pass.  Rows, weights, outputs
  * and workspaces of these calls begin at multiples of 16 bytes (MOE_ERR_ARG
- * otherwise); d and I are below 2^22, beside moe.h's limits.
+ * otherwise).  Limits beside moe.h's: d and I below 2^22, E * 2*d*I below 2^34;
+ * one expert's 2*d*I below 2^30 where the weights come in moe.h's layouts
+ * (moe_quantize_weights, moe_forward_few), below 2^31 where they come as 8-bit
+ * codes.
  *
  * The 8-bit format.  A code is e4m3 (OCP: sign, 4 bits of exponent with bias
  * 7, 3 of mantissa; largest 448, no infinities, 0x7F and 0xFF are NaN).  A
@@ -66,9 +69,8 @@ moe_status moe_quantize_weights(const void* w_gate_up, const void* w_down, moe_d
  *     row_token[r] (as moe_permute writes it; a row outside [0, x_rows) is
  *     read as zeros)
  *   h_q [max_rows, I] e4m3, h_s [max_rows, ceil(I/128)];  y_perm [max_rows, d] bf16
- * Limits as moe.h's; x_rows * d, max_rows * max(d, I) and one expert's 2*d*I
- * below 2^31.  moe_grouped_ffn_fp8 needs moe_grouped_ffn_fp8_workspace_size()
- * bytes for h.                                                             */
+ * x_rows * d and max_rows * max(d, I) below 2^31.  moe_grouped_ffn_fp8 needs
+ * moe_grouped_ffn_fp8_workspace_size() bytes for h.                        */
 moe_status moe_gate_up_swiglu_fp8(const void* x_q, const float* x_s, const int32_t* expert_offsets, int32_t max_rows,
                                   int32_t E, int32_t d, int32_t I, const void* w_gate_up_q, const float* w_gate_up_s,
                                   const int32_t* row_token, int32_t x_rows, void* h_q, float* h_s, void* stream);

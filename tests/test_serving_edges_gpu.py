@@ -1,5 +1,6 @@
 """The serving operators on the GPU at the ends of their ranges: gates whose
-SwiGLU factors leave float32 though the product does not."""
+SwiGLU factors leave float32 though the product does not, and layers whose
+weights pass 2^31 bytes."""
 import numpy as np
 import pytest
 
@@ -44,3 +45,102 @@ def test_gate_up_extreme_gates(tre, rows):
     # float32's normal range; where the denominator passes it, |silu| <= 88.73 e^-88.73 = 2.7e-37 may become zero
     bound = 8 * ref.HALF_F32 * np.abs(h) + 1e-37 + np.where(g < -88.72, 2.7e-37, 0.0)[:, None] * np.abs(ups)
     check_codes(hq, hs, h, bound, f"{rows} rows an expert")
+
+
+# ---- layers whose weights pass 2^31 bytes -------------------------------------------------------
+
+BIG_E, BIG_D, BIG_I = 3, 16384, 40960     # 1.34e9 gate/up codes an expert, 4.0e9 in all
+
+
+@pytest.fixture(scope="module")
+def big(tre):
+    """Codes +-0.5 and +-1 and scales 0.5 and 1: every product is a multiple of 2^-4, and a sum over the widest side
+    stays below 2^16, so float32 sums are exact in any order."""
+    torch = T()
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def codes(*shape):
+        q = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+        return q.bitwise_and_(0x88).bitwise_or_(0x30).view(torch.float8_e4m3fn)
+
+    def scales(*shape):
+        return torch.randint(1, 3, shape, device="cuda", generator=g).float() * 0.5
+
+    nb, db = ref.blocks(BIG_I), ref.blocks(BIG_D)
+    yield codes, scales, (codes(BIG_E, 2 * BIG_I, BIG_D), scales(BIG_E, 2, nb, db), codes(BIG_E, BIG_D, BIG_I),
+                          scales(BIG_E, db, nb))
+    torch.cuda.empty_cache()
+
+
+def spread64(q, s, rows=1):
+    """What codes [n, k] and scales [n / rows, k / 128] stand for, in 64 bits."""
+    s = s.double().repeat_interleave(128, 1)[:, :q.shape[1]].repeat_interleave(rows, 0)[:q.shape[0]]
+    return q.float().double() * s
+
+
+def times(a, q, s, mul=lambda w: w):
+    """a [n, K] @ mul(w) of one expert's [N, K] codes, in pieces of whole blocks."""
+    return T().cat([a @ mul(spread64(q[n:n + 4096], s[n // 128:n // 128 + 32], 128)).t().contiguous()
+                    for n in range(0, q.shape[0], 4096)], 1)
+
+
+def gate_up64(a, w, e, mul=lambda w: w):
+    return T().cat([times(a, w[0][e, i * BIG_I:(i + 1) * BIG_I], w[1][e, i], mul) for i in (0, 1)], 1)
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 5], [500, 30, 700]], ids=["low_tiles", "high_tiles"])
+def test_products_past_two_gib(tre, big, counts):
+    torch = T()
+    codes, scales, w = big
+    R, offs = sum(counts), offsets_of(counts)
+    xq, xs = codes(R, BIG_D), scales(R, ref.blocks(BIG_D)) * 0.25
+    hq, hs = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w[0], w[1])
+    aq, as_ = codes(R, BIG_I), scales(R, ref.blocks(BIG_I))
+    y = tre.moe_down_proj_fp8(aq, as_, offs, w[2], w[3])
+    at = 0
+    for e, n in enumerate(counts):
+        rows = torch.unique(torch.linspace(at, at + n - 1, min(n, 6), device="cuda").long()) if n else []
+        at += n
+        if not n:
+            continue
+        exact = times(spread64(aq.view(torch.uint8)[rows].view(aq.dtype), as_[rows]), w[2][e], w[3][e])
+        assert torch.equal(y[rows], exact.float().to(torch.bfloat16)), (e, n)
+        gu = gate_up64(spread64(xq.view(torch.uint8)[rows].view(xq.dtype), xs[rows]), w, e).cpu().numpy()
+        h, eh = ref.swiglu(gu, np.zeros_like(gu))
+        check_codes(hq.view(torch.uint8)[rows].view(hq.dtype), hs[rows], h, eh, f"expert {e} of {counts}")
+    whole = tre.moe_grouped_ffn_fp8(xq, xs, offs, *w)
+    assert torch.equal(whole, tre.moe_down_proj_fp8(hq, hs, offs, w[2], w[3]))
+
+
+def test_few_tokens_past_two_gib(tre, big):
+    torch = T()
+    _, _, w = big
+    ids, T_, k = np.array([[0, 2], [2, -1], [1, 2]], np.int32), 3, 2
+    wts = np.random.default_rng(2).random((T_, k)).astype(np.float32)
+    x = torch.randn((T_, BIG_D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3)).mul(0.01)
+    x = x.to(torch.bfloat16)
+    out, _, _ = tre.moe_forward_few_fp8(x, *w, k, topk_idx=to_device(ids), topk_w=to_device(wts))
+    want, err, size = (np.zeros((T_, BIG_D)) for _ in range(3))
+    for e in range(BIG_E):
+        t, j = np.nonzero(ids == e)
+        xe = x[torch.from_numpy(t).cuda()].double()
+        # as serving_ref.layer bounds it: a float32 step for each addition and each block's scale, h and the output
+        # rounded to bf16
+        step = (BIG_D + 3 * ref.blocks(BIG_D)) * ref.SUM
+        h, eh = ref.swiglu(gate_up64(xe, w, e).cpu().numpy(), step * gate_up64(xe.abs(), w, e, torch.abs).cpu().numpy())
+        eh = eh + ref.HALF_BF16 * (np.abs(h) + eh)
+        h, eh = torch.from_numpy(h).cuda(), torch.from_numpy(eh).cuda()
+        step = (BIG_I + 19 * ref.blocks(BIG_I)) * ref.SUM
+        y = times(h, w[2][e], w[3][e]).cpu().numpy()
+        ey = times(step * h.abs() + eh, w[2][e], w[3][e], torch.abs).cpu().numpy()
+        wt = wts[t, j].astype(np.float64)[:, None]
+        np.add.at(want, t, wt * y)
+        np.add.at(err, t, wt * ey)
+        np.add.at(size, t, np.abs(wt * y))
+    err = err + (k + 1) * ref.SUM * size
+    tol = err + ref.HALF_BF16 * (np.abs(want) + err)
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+    # the roundings of h are independent of each other and of the weights' signs, so in the norm they add in
+    # quadrature and make at most a half step of y; the output's rounding makes another
+    assert np.linalg.norm(got - want) <= 2 * ref.HALF_BF16 * np.linalg.norm(want)

@@ -20,14 +20,17 @@ bool aligned16(const P*... p) {
 // A row tile of 288 rows of 8-bit codes is addressed with 31 bits.
 constexpr int32_t kMaxWidth = 1 << 22;
 
-// E experts of widths d and I.
-moe_status check_layer(int32_t E, int32_t d, int32_t I) {
+// E experts of widths d and I, whose gate/up weights are of `size` bytes an
+// element: one expert's stay below 2 GiB, the reach of one buffer descriptor
+// (2 for the calls that take weights in moe.h's layouts, which are refused
+// where moe.h's calls refuse them, float32 or not; 1 for 8-bit codes).
+moe_status check_layer(int32_t E, int32_t d, int32_t I, int32_t size) {
   TRY(check_experts(E));
   TRY(check_width(d));
   TRY(check_width(I));
   if (d >= kMaxWidth || I >= kMaxWidth) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)E * d * 2 * I >= 8 * kMaxElems) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)d * I * 4 >= kMaxElems) return MOE_ERR_UNSUPPORTED;   // one expert's bf16 gate/up weights < 2 GiB
+  if ((int64_t)d * I * 2 * size >= kMaxElems) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -51,9 +54,9 @@ bool few_sizes_ok(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I) {
 }
 
 moe_status check_few(const void* x, const float* logits, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I,
-                     const int32_t* topk_idx, const float* topk_w, const void* out) {
+                     int32_t size, const int32_t* topk_idx, const float* topk_w, const void* out) {
   if (T < 0 || k < 1) return MOE_ERR_ARG;
-  TRY(check_layer(E, d, I));
+  TRY(check_layer(E, d, I, size));
   if (logits && k > E) return MOE_ERR_ARG;
   if (T > kFewTokens || (int64_t)T * k > kFewPairs) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
@@ -110,7 +113,7 @@ Forward8Layout forward8_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64
 
 moe_status check_rows8(int32_t max_rows, int32_t E, int32_t d, int32_t I) {
   if (max_rows < 0) return MOE_ERR_ARG;
-  TRY(check_layer(E, d, I));
+  TRY(check_layer(E, d, I, 1));
   if ((int64_t)max_rows * (d > I ? d : I) >= kMaxElems) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -141,7 +144,7 @@ moe_status moe_quantize_weights(const void* w_gate_up, const void* w_down, moe_d
                                 int32_t I, void* w_gate_up_q, float* w_gate_up_s, void* w_down_q, float* w_down_s,
                                 void* stream) {
   if (!dtype_ok(dt)) return MOE_ERR_ARG;
-  TRY(check_layer(E, d, I));
+  TRY(check_layer(E, d, I, 2));
   if (!w_gate_up || !w_down || !w_gate_up_q || !w_gate_up_s || !w_down_q || !w_down_s) return MOE_ERR_ARG;
   if (!aligned16(w_gate_up, w_down, w_gate_up_q, w_down_q)) return MOE_ERR_ARG;
   hipStream_t s = (hipStream_t)stream;
@@ -218,7 +221,7 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
                            int32_t* row_token, int32_t* pair_row, void* out, void* workspace, size_t workspace_bytes,
                            void* stream) {
   if (T < 0 || k < 1) return MOE_ERR_ARG;
-  TRY(check_layer(E, d, I));
+  TRY(check_layer(E, d, I, 1));
   if (logits && k > E) return MOE_ERR_ARG;
   const int64_t P = (int64_t)T * k;
   if (P * (d > I ? d : I) >= kMaxElems || (int64_t)T * E >= kMaxElems) return MOE_ERR_UNSUPPORTED;
@@ -258,7 +261,7 @@ moe_status moe_forward_few(const void* x, const float* logits, int32_t T, int32_
                            const void* w_gate_up, const void* w_down, moe_dtype dt, int32_t* topk_idx, float* topk_w,
                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dt)) return MOE_ERR_ARG;
-  TRY(check_few(x, logits, T, d, E, k, I, topk_idx, topk_w, out));
+  TRY(check_few(x, logits, T, d, E, k, I, 2, topk_idx, topk_w, out));
   if (T == 0) return MOE_OK;
   if (!w_gate_up || !w_down || !aligned16(x, w_gate_up, w_down, out, workspace)) return MOE_ERR_ARG;
   const int split = dt == MOE_BF16 ? few_split_bf16(T * k, E, d, I) : few_split_f32(T * k, E, d, I);
@@ -282,7 +285,7 @@ moe_status moe_forward_few_fp8(const void* x, const float* logits, int32_t T, in
                                int32_t I, const void* w_gate_up_q, const float* w_gate_up_s, const void* w_down_q,
                                const float* w_down_s, int32_t* topk_idx, float* topk_w, void* out, void* workspace,
                                size_t workspace_bytes, void* stream) {
-  TRY(check_few(x, logits, T, d, E, k, I, topk_idx, topk_w, out));
+  TRY(check_few(x, logits, T, d, E, k, I, 1, topk_idx, topk_w, out));
   if (T == 0) return MOE_OK;
   if (!w_gate_up_q || !w_gate_up_s || !w_down_q || !w_down_s) return MOE_ERR_ARG;
   if (!aligned16(x, w_gate_up_q, w_down_q, out, workspace)) return MOE_ERR_ARG;
