@@ -144,3 +144,23 @@ def test_few_tokens_past_two_gib(tre, big):
     # the roundings of h are independent of each other and of the weights' signs, so in the norm they add in
     # quadrature and make at most a half step of y; the output's rounding makes another
     assert np.linalg.norm(got - want) <= 2 * ref.HALF_BF16 * np.linalg.norm(want)
+
+
+# ---- the binding ------------------------------------------------------------------------------------
+
+def test_max_rows_without_row_token(tre):
+    """Without row_token the rows are x_q's: another max_rows is refused, not passed over."""
+    torch = T()
+    f8 = torch.float8_e4m3fn
+    xq, xs = torch.ones((6, 64), device="cuda").to(f8), torch.ones((6, 1), device="cuda")
+    w, ws = torch.ones((2, 128, 64), device="cuda").to(f8), torch.ones((2, 2, 1, 1), device="cuda")
+    offs = offsets_of([2, 4])
+    for rows in (0, 4, 7):
+        with pytest.raises(ValueError, match="max_rows"):
+            tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w, ws, max_rows=rows)
+    a = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w, ws, max_rows=6)
+    token = to_device(np.arange(6, dtype=np.int32))
+    b = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w, ws, row_token=token)
+    c = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w, ws, row_token=token, max_rows=5)
+    assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+    assert c[0].shape == (5, 64) and c[1].shape == (5, 1)

@@ -655,7 +655,7 @@ def moe_gate_up_swiglu_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, h
                            max_rows=None, stream=None):
     """moe_gate_up_swiglu on 8-bit rows (x_q, x_s from moe_quantize_rows) and weights -> (h_q [R, I], h_s
     [R, ceil(I/128)]).  With ``row_token`` [R], row r is x's row row_token[r]; R = ``max_rows`` (default
-    len(row_token))."""
+    len(row_token)).  Without, R is x_q's number of rows, and another ``max_rows`` is refused."""
     torch = _torch()
     lib = load()
     x_rows, d = x_q.shape
@@ -663,7 +663,10 @@ def moe_gate_up_swiglu_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, h
     f8, f32 = torch.float8_e4m3fn, torch.float32
     px, ps = c.tensor(x_q, f8, (x_rows, d), "x_q"), c.tensor(x_s, f32, (x_rows, _blocks(d)), "x_s")
     R, pt = x_rows, None
-    if row_token is not None:
+    if row_token is None:
+        if max_rows is not None and max_rows != x_rows:
+            raise ValueError(f"max_rows {max_rows} without row_token: x_q has {x_rows} rows")
+    else:
         R = int(max_rows if max_rows is not None else row_token.shape[0])
         pt = c.tensor(row_token, torch.int32, (row_token.shape[0],), "row_token")
         if row_token.shape[0] < R:
