@@ -6,7 +6,7 @@ import pytest
 
 import serving_ref as ref
 from helpers import to_device
-from test_serving_gpu import T, check_codes, offsets_of, sync, tre   # noqa: F401 (tre: the fixture)
+from test_serving_gpu import T, check_codes, few_call, few_weights, offsets_of, rand, routed, sync, tre   # noqa: F401 (tre: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,22 @@ def test_max_rows_without_row_token(tre):
     c = tre.moe_gate_up_swiglu_fp8(xq, xs, offs, w, ws, row_token=token, max_rows=5)
     assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
     assert c[0].shape == (5, 64) and c[1].shape == (5, 1)
+
+
+@pytest.mark.parametrize("form", ["bf16", "f32", "fp8", "layer8"])
+def test_flat_pairs(tre, form):
+    """Pairs as moe_permute takes them, [T * k] instead of [T, k], as moe_forward does; another length is refused."""
+    torch = T()
+    T_, d, E, k, I = 5, 128, 4, 2, 64
+    w, _, _ = few_weights("fp8" if form == "layer8" else form, E, d, I, 200)
+    x, _ = rand((T_, d), "f32" if form == "f32" else "bf16", 201)
+    call = (lambda **kw: tre.moe_forward_fp8(x, *w, k, **kw)) if form == "layer8" else \
+        (lambda **kw: few_call(tre, form, x, w, k, **kw))
+    idx, wt = tre.moe_route_topk(routed(T_, E, k, 202)[0], k)
+    want = call(topk_idx=idx, topk_w=wt)[0]
+    out, i2, w2 = call(topk_idx=idx.reshape(-1), topk_w=wt.reshape(-1))
+    sync()
+    assert torch.equal(out, want) and i2.shape == (T_ * k,) and w2.shape == (T_ * k,)
+    for i, v in ((idx.reshape(-1)[1:], wt), (idx, wt.reshape(-1)[1:]), (idx.reshape(k, T_), wt)):
+        with pytest.raises(ValueError):
+            call(topk_idx=i, topk_w=v)

@@ -647,8 +647,10 @@ def _routing(c, logits, topk_idx, topk_w, T, E, k):
         topk_w = c.empty((T, k), torch.float32) if topk_w is None else topk_w
     elif topk_idx is None or topk_w is None:
         raise ValueError("without logits, topk_idx and topk_w must be given")
-    return (plg, topk_idx, topk_w, c.tensor(topk_idx, torch.int32, (T, k), "topk_idx"),
-            c.tensor(topk_w, torch.float32, (T, k), "topk_w"))
+    # as moe_forward, given pairs may also come flat, [T * k]
+    return (plg, topk_idx, topk_w,
+            c.tensor(topk_idx, torch.int32, (T, k) if topk_idx.dim() != 1 else (T * k,), "topk_idx"),
+            c.tensor(topk_w, torch.float32, (T, k) if topk_w.dim() != 1 else (T * k,), "topk_w"))
 
 
 def moe_gate_up_swiglu_fp8(x_q, x_s, expert_offsets, w_gate_up_q, w_gate_up_s, h_q=None, h_s=None, row_token=None,
