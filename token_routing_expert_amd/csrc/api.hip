@@ -490,7 +490,6 @@ moe_status moe_backward(const void* x, const float* logits, int32_t T, int32_t d
 
   char* ws = (char*)workspace;
   int32_t* p_row = (int32_t*)(ws + L.pair_row);
-  int32_t* r_tok = (int32_t*)(ws + L.row_token);
   int32_t* offs = (int32_t*)(ws + L.offsets);
   bf16_t* x_perm = (bf16_t*)(ws + L.x_perm);
   bf16_t* h = (bf16_t*)(ws + L.h);

@@ -204,7 +204,6 @@ struct Blocked8 {
 
 // ---- the parts the two kernels share ------------------------------------------
 
-__device__ __forceinline__ float few_load(const bf16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void few_store(bf16_t* p, float f) { *p = f32_to_bf16(f); }
 __device__ __forceinline__ void few_store(float* p, float f) { *p = f; }
 __device__ __forceinline__ void few_store4(bf16_t* p, f32x4 f) {
