@@ -6,12 +6,12 @@
  * pointers, work enqueued on `stream`, arguments checked on the host first,
  * nothing allocated, values read on the device clamped to what they index).
  *
- * Inference only: none of these has a backward pass.  Rows, weights, outputs
- * and workspaces of these calls begin at multiples of 16 bytes (MOE_ERR_ARG
- * otherwise).  Limits beside moe.h's: d and I below 2^22, E * 2*d*I below 2^34;
- * one expert's 2*d*I below 2^30 where the weights come in moe.h's layouts
- * (moe_quantize_weights, moe_forward_few), below 2^31 where they come as 8-bit
- * codes.
+ * Inference only: none of these has a backward pass.  Rows, codes, weights,
+ * `out` and workspaces begin at multiples of 16 bytes (MOE_ERR_ARG otherwise);
+ * scales, indices and routing weights at multiples of their own 4.  Limits
+ * beside moe.h's: d and I below 2^22, E * 2*d*I below 2^34; one expert's 2*d*I
+ * below 2^30 where the weights come in moe.h's layouts (moe_quantize_weights,
+ * moe_forward_few), below 2^31 where they come as 8-bit codes.
  *
  * The 8-bit format.  A code is e4m3 (OCP: sign, 4 bits of exponent with bias
  * 7, 3 of mantissa; largest 448, no infinities, 0x7F and 0xFF are NaN).  A
@@ -61,9 +61,18 @@ moe_status moe_quantize_weights(const void* w_gate_up, const void* w_down, moe_d
  * weights.  For row r of expert e and output column n:
  *   sum over blocks b of xs[r, b] * ws[e, n/128, b] *
  *       (sum over k in block b of xq[r, k] * wq[e, n, k])
- * in float32, blocks in ascending order.  gate_up quantises
- * h = silu(gate) * up as moe_quantize_rows does, from float32; down rounds its
- * sum to bf16 once.  Rows >= expert_offsets[E] of the outputs are untouched.
+ * blocks in ascending order, in float32 from a block's sum on.  gate_up
+ * quantises h = silu(gate) * up as moe_quantize_rows does, from float32; down
+ * rounds its sum to bf16 once.  Rows >= expert_offsets[E] of the outputs are
+ * untouched.
+ *   The sum within a block is float32 only in gate_up with few rows an expert
+ * (tiles of up to 64 rows).  Elsewhere the 8-bit matrix instruction forms it:
+ * of every 8 consecutive products it drops what lies 13 binary places below the
+ * largest, less than 7 * 2^-13 of that product for each group of 8.  Which of
+ * the two a row meets follows from the call's sizes (max_rows / E, E, d, I), so
+ * equal calls give equal bits, but a row's y may differ in its last places, and
+ * codes of its h, when other rows share the call: the same prompt whole and in
+ * pieces agrees within that bound, not bit for bit.
  *   x_q [x_rows, d] e4m3, x_s [x_rows, ceil(d/128)];  row_token: NULL (row r
  *     is x's row r, and x_rows is not read) or [max_rows], row r is x's row
  *     row_token[r] (as moe_permute writes it; a row outside [0, x_rows) is
@@ -97,9 +106,11 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
  * moe_forward for a decode step, in two kernels: routing, grouping, the row
  * gather and gate/up + SwiGLU in the first, the down projection and the
  * combine in the second.  Only the weights of experts that have rows are
- * read, once for every 64 rows of one (8-bit: 32).  The selection and the routing weights
- * are moe_route_topk's bit for bit; the products' sums run in another order
- * than moe_forward's (float32; h rounded to dt; the experts' outputs are
+ * read, once for every 16 rows of one with T <= 16, 32 with T <= 32 and 64
+ * above (8-bit: 32): once, where no token names an expert twice, but for 8-bit
+ * weights of an expert with more than 32 rows.  The selection and the routing
+ * weights are moe_route_topk's bit for bit; the products' sums run in another
+ * order than moe_forward's (float32; h rounded to dt; the experts' outputs are
  * summed before they are rounded, once).  The order of every sum depends on
  * the sizes only, so equal calls give equal bits.
  *   1 <= T <= MOE_FEW_MAX_TOKENS and T * k <= MOE_FEW_MAX_PAIRS, else
@@ -109,7 +120,15 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
  *   calls that may overlap need workspaces of their own
  * moe_forward_few_fp8 is the same on 8-bit weights, with bf16 x and out: the
  * activations and h stay in bf16 (the weights' bytes are what a few tokens
- * cost, and exact activations are free beside them).                       */
+ * cost, and exact activations are free beside them).
+ *   Which call for T <= 64, measured with cold weights on layers of 16 experts,
+ * 1024 x 2816 and 5120 x 8192, and of 128, 2880 x 2880: in float32 and bf16 the
+ * few-token call (64 tokens, 128 experts: 867 us, moe_forward 1022; one token
+ * 47 and 115); only on the widest layer is it up to 11% behind moe_forward_tiled
+ * (8 tokens, 371 and 333 us).  On 8-bit weights the few-token call up to 16
+ * tokens (8 tokens, 128 experts: 147 us, moe_forward_fp8 182), and above where
+ * the layer is small; on the wide ones moe_forward_fp8 is level at 32 (428 and
+ * 431) and ahead at 64 (603 and 575), with activations in 8 bits.           */
 #define MOE_FEW_MAX_TOKENS 64
 #define MOE_FEW_MAX_PAIRS 1024
 size_t moe_forward_few_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt);

@@ -1,12 +1,14 @@
 """The serving operators on the GPU at the ends of their ranges: gates whose
-SwiGLU factors leave float32 though the product does not, and layers whose
-weights pass 2^31 bytes."""
+SwiGLU factors leave float32 though the product does not, layers whose weights
+pass 2^31 bytes, the same rows in calls of different sizes, and what the
+binding takes and refuses."""
 import numpy as np
 import pytest
 
 import serving_ref as ref
 from helpers import to_device
-from test_serving_gpu import T, check_codes, few_call, few_weights, offsets_of, rand, routed, sync, tre   # noqa: F401 (tre: the fixture)
+from test_serving_gpu import (T, check_codes, few_call, few_weights, offsets_of, product_tolerance, rand, random_codes,   # noqa: F401
+                              random_scales, routed, sync, tre, weights8)   # (tre: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -144,6 +146,40 @@ def test_few_tokens_past_two_gib(tre, big):
     # the roundings of h are independent of each other and of the weights' signs, so in the norm they add in
     # quadrature and make at most a half step of y; the output's rounding makes another
     assert np.linalg.norm(got - want) <= 2 * ref.HALF_BF16 * np.linalg.norm(want)
+
+
+# ---- the same rows in calls of different sizes ----------------------------------------------------
+
+def test_rows_alone_and_among_others(tre):
+    """Tiles of other heights sum a block in other arithmetic: what a row gives in a small call and in a large one
+    stays within the header's bound of the exact value, so within twice that of each other."""
+    torch = T()
+    E, d, I, n, more = 16, 576, 2048, 8, 300
+    w, wgu, wd = weights8(E, d, I, 210)
+    few, many = offsets_of([n] * E), offsets_of([more] * E)
+    pick = torch.cat([torch.arange(n) + e * more for e in range(E)]).cuda()
+    xq, xs = random_codes((E * more, d), 211), random_scales((E * more, ref.blocks(d)), 212, 0.002, 0.02)
+    aq, as_ = random_codes((E * more, I), 213), random_scales((E * more, ref.blocks(I)), 214, 0.01, 0.02)
+
+    def picked(q, s):
+        return q.view(torch.uint8)[pick].view(q.dtype), s[pick]
+
+    (xq1, xs1), (aq1, as1) = picked(xq, xs), picked(aq, as_)
+    small = tre.moe_gate_up_swiglu_fp8(xq1, xs1, few, w[0], w[1])
+    large = picked(*tre.moe_gate_up_swiglu_fp8(xq, xs, many, w[0], w[1]))
+    y1 = tre.moe_down_proj_fp8(aq1, as1, few, w[2], w[3])
+    y2 = tre.moe_down_proj_fp8(aq, as_, many, w[2], w[3])[pick]
+    sync()
+    x, a = ref.row_values(xq1, xs1), ref.row_values(aq1, as1)
+    for e in range(E):
+        r = slice(e * n, (e + 1) * n)
+        check_codes(small[0][r], small[1][r], *ref.swiglu(*ref.product(x[r], wgu[e], 3)), f"few rows, expert {e}")
+        check_codes(large[0][r], large[1][r], *ref.swiglu(*ref.product(x[r], wgu[e], 3, codes8=True)),
+                    f"many rows, expert {e}")
+        want, bound = ref.product(a[r], wd[e], 3, codes8=True)
+        tol = product_tolerance(want, bound)
+        for y in (y1, y2):
+            assert np.all(np.abs(y[r].double().cpu().numpy() - want) <= tol), e
 
 
 # ---- the binding ------------------------------------------------------------------------------------
