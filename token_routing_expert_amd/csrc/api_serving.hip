@@ -236,7 +236,7 @@ moe_status moe_forward_fp8(const void* x, const float* logits, int32_t T, int32_
   int32_t* p_row = pair_row ? pair_row : (int32_t*)(ws + L.pair_row);
   int32_t* r_tok = row_token ? row_token : (int32_t*)(ws + L.row_token);
   int32_t* offs = expert_offsets ? expert_offsets : (int32_t*)(ws + L.offsets);
-  bf16_t* y = (bf16_t*)(ws + L.y);
+  bf16_t* y = (bf16_t*)(ws + L.y);   // rounded once before the combine, as moe_forward's: half the bytes of float32
   const Ffn8Layout F = ffn8_layout(P, I);
   uint8_t* h_q = (uint8_t*)(ws + L.ffn + F.h_q);
   float* h_s = (float*)(ws + L.ffn + F.h_s);

@@ -19,6 +19,9 @@
 // 128 experts, 2880 x 2880, bf16 24.8 + 17.4 us, 4.7 TB/s; 64 tokens, 1 of 16,
 // 5120 x 8192, bf16 454 + 227 us, 5.9 TB/s; 8 tokens, 4 of 128, 8 bits 96 + 52
 // us, 4.8 TB/s; 3 tokens of a 128 x 256 float32 layer 5.7 + 7.0 us, all latency.
+// With many live experts the 8-bit weights stream at 4.4 to 4.6 TB/s, the grouped
+// products' at 4.8 to 5.0, so from about 32 tokens on those are ahead (64 tokens, 4
+// of 128, cold: 603 us, moe_forward_fp8 575; 1 of 16, 5120 x 8192: 456 and 398).
 //
 // The order of k inside a matrix instruction is free as long as both operands
 // use the same: each policy below lets a lane's 16-byte weight loads run along
@@ -432,6 +435,8 @@ __global__ __launch_bounds__(M::kGuWaves * kWave) void k_few_gate_up(
           const int row = i / CT, c = i % CT, r = r0 + m * 16 + row;
           if (r >= n) break;   // rows ascend with i
           const float gate = few_sum<M, NW>(red, row, M::gate_slot(c)), up = few_sum<M, NW>(red, row, M::up_slot(c));
+          // h is an operand of the second kernel's matrix instructions, so it is
+          // rounded to their type here, once (float32 layers keep it whole)
           few_store(h + (int64_t)g.list[r] * I + n0 + c, gate / (1.f + expf(-gate)) * up);
         }
       }

@@ -6,8 +6,9 @@
 // One matrix instruction covers a block of k, so a block's sums leave it
 // unscaled (its addend is the constant zero) and are added to the float32
 // accumulators with one multiplied-add an element: four vector instructions
-// beside each matrix instruction of 32 cycles, in the shadow of the other
-// waves' matrix work.
+// beside each matrix instruction of 32 cycles.  Most of them run beside the
+// other waves' matrix work, not all (32768 rows, 16 experts, 2880 x 2880: 372
+// us, without them 330).
 //
 // Tile: BM rows x BN weight rows, one block of 128 bytes of k a stage, both
 // operands loaded straight to LDS (16-byte chunk c of row r in slot
@@ -35,12 +36,16 @@
 //     of 128 experts, 2880 x 2880: 856 us, in bf16 1423; 1024 rows, 16 experts,
 //     1024 x 2816: 30.6 and 40.2; both before weights came two stages ahead),
 //     0.22% to 0.45% off over forty shapes.
-// Measured: down, 64 rows, 16 experts, 8192 x 5120: 124 us, 5.4 TB/s of weights;
-// 32768 rows, 16 experts, 2880 x 2880: 349 us, 1.56 PFLOP/s; gate/up of 32768
-// rows, 128 experts, 2880 x 2880: 806 us in the layer, 1.35 PFLOP/s.  With the
-// loads dropped the 32768-row product took 247 us, with the matrix instructions
-// dropped 296, loads alone 283: the three wait for each other at the stages'
-// barriers.
+// Measured in streams of calls, two sets of inputs and weights in turn: down, 64
+// rows, 16 experts, 8192 x 5120: 122 us, 5.5 TB/s of weights; 32768 rows, 16
+// experts, 2880 x 2880: 349 to 367 us on four cards, 1.5 PFLOP/s; gate/up of 64
+// rows, 16 experts, 2880 x 2880: 63 us, 4.2 TB/s of weights; of 32768 rows, 128
+// experts, 2880 x 2880: 806 to 822 us, 1.34 PFLOP/s.  A call by itself takes up
+// to 10% longer (the 32768-row product 375 to 406 us).  Where two forms are
+// compared, here and below, both ran on one card and the same inputs, which
+// repeat, so that weights partly come from the last-level cache.  With the loads dropped the 32768-row product took 247 us, with the
+// matrix instructions dropped 296, loads alone 283, all 372: the three wait for
+// each other at the stages' barriers.
 // XCDs: consecutive tiles go to one XCD, in groups of up to 8 row tiles for
 // each weight slice, so that a slice is fetched once for the group and the
 // group's rows stay in that XCD's L2.
@@ -647,8 +652,9 @@ hipError_t down8(const Gemm8Args& g, hipStream_t s) {
     case 64: return gemm8<false, 64, 128, 1, 2>(g, s);
     case 128:
       // 160 where the rows over a multiple of 128 would leave most units idle in
-      // the last round (8192 rows, 16 experts, 2816 x 1024: 34 us, 128 rows
-      // 43.5; 4096 rows 24 and 28; but 6144 rows 31.5 and 29, 10240 48 and 44)
+      // the last round (8192 rows, 16 experts, 2816 x 1024, on one card: 34 us,
+      // 128 rows 43.5; 4096 rows 24 and 28; but 6144 rows 31.5 and 29, 10240 48
+      // and 44; by the rows' spread over the experts, 8192 take up to 41)
       if (longest_walk(g, 160, 128) < longest_walk(g, 128, 128)) return gemm8<false, 160, 128, 2, 2>(g, s);
       return gemm8<false, 128, 128, 2, 2>(g, s);
     default: return gemm8<false, 288, 256, 2, 2>(g, s);
