@@ -219,3 +219,18 @@ def test_flat_pairs(tre, form):
     for i, v in ((idx.reshape(-1)[1:], wt), (idx, wt.reshape(-1)[1:]), (idx.reshape(k, T_), wt)):
         with pytest.raises(ValueError):
             call(topk_idx=i, topk_w=v)
+
+
+@pytest.mark.parametrize("form", ["bf16", "f32", "fp8", "layer8"])
+@pytest.mark.parametrize("given", [False, True])
+def test_no_tokens(tre, form, given):
+    """An empty batch, as the last step of a server may hold: empty outputs, whatever allocates them."""
+    torch = T()
+    d, E, k, I = 128, 4, 2, 64
+    w, _, _ = few_weights("fp8" if form == "layer8" else form, E, d, I, 220)
+    x = torch.empty((0, d), dtype=torch.float32 if form == "f32" else torch.bfloat16, device="cuda")
+    kw = dict(topk_idx=torch.empty((0, k), dtype=torch.int32, device="cuda"), topk_w=torch.empty((0, k), device="cuda")) \
+        if given else dict(logits=torch.empty((0, E), device="cuda"))
+    out, idx, wt = tre.moe_forward_fp8(x, *w, k, **kw) if form == "layer8" else few_call(tre, form, x, w, k, **kw)
+    sync()
+    assert out.shape == (0, d) and idx.shape == (0, k) and wt.shape == (0, k)

@@ -52,3 +52,19 @@ def test_weights_in_sixteen_bits():
     assert answers(lib, 1, 16384, 32768 - 64)[1] == WORKSPACE
     assert answers(lib, 1, 16384, 32768)[1] == UNSUPPORTED
     assert lib.moe_quantize_weights(F, F, 1, 1, 16384, 32768, F, F, F, F, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (16, 2), (256, 1), (4, 256)])
+def test_no_tokens(E, k):
+    """Zero tokens are valid: every workspace has a size, and every call nothing to do."""
+    lib, d, I = tre.load(), 128, 192
+    sizes = [lib.moe_forward_fp8_workspace_size(0, d, E, k, I), lib.moe_forward_few_fp8_workspace_size(0, d, E, k, I)]
+    sizes += [lib.moe_forward_few_workspace_size(0, d, E, k, I, dt) for dt in (0, 1)]
+    assert all(0 < n <= lib.moe_forward_fp8_workspace_size(1, d, E, k, I) for n in sizes)
+    assert lib.moe_grouped_ffn_fp8_workspace_size(0, I) == 0
+    for dt in (0, 1):
+        assert lib.moe_forward_few(None, None, 0, d, E, k, I, FAKE, FAKE, dt, None, None, None, None, 0, None) == OK
+    assert lib.moe_forward_few_fp8(None, None, 0, d, E, k, I, FAKE, FAKE, FAKE, FAKE, None, None, None, None, 0,
+                                   None) == OK
+    assert lib.moe_forward_fp8(None, None, 0, d, E, k, I, FAKE, FAKE, FAKE, FAKE, None, None, None, None, None, None,
+                               None, 0, None) == OK

@@ -547,6 +547,7 @@ constexpr int kFewCus = 256, kFewWaves = 16;   // compute units, and waves that 
 // wave keeps two steps of its own.
 template <class M>
 int few_split(int P, int E, int d, int I) {
+  if (P == 0) return 1;   // no tokens: a workspace is asked for all the same
   const int64_t tiles = ceil_div(d, M::kCols) * (P < E ? P : E);
   const int steps = (int)ceil_div(I, M::kStep);
   int64_t n = ceil_div(128, tiles);
