@@ -1,14 +1,14 @@
 """The serving operators on the GPU at the ends of their ranges: gates whose
 SwiGLU factors leave float32 though the product does not, layers whose weights
-pass 2^31 bytes, the same rows in calls of different sizes, and what the
-binding takes and refuses."""
+pass 2^31 bytes, the widest layers and the most experts, the same rows in calls
+of different sizes, and what the binding takes and refuses."""
 import numpy as np
 import pytest
 
 import serving_ref as ref
 from helpers import to_device
-from test_serving_gpu import (T, check_codes, few_call, few_weights, offsets_of, product_tolerance, rand, random_codes,   # noqa: F401
-                              random_scales, routed, sync, tre, weights8)   # (tre: the fixture)
+from test_serving_gpu import (T, check_codes, few_call, few_weights, offsets_of, product_tolerance,   # noqa: F401
+                              rand, random_codes, random_scales, routed, sync, tre, weights8)   # (tre: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -229,8 +229,94 @@ def test_no_tokens(tre, form, given):
     d, E, k, I = 128, 4, 2, 64
     w, _, _ = few_weights("fp8" if form == "layer8" else form, E, d, I, 220)
     x = torch.empty((0, d), dtype=torch.float32 if form == "f32" else torch.bfloat16, device="cuda")
-    kw = dict(topk_idx=torch.empty((0, k), dtype=torch.int32, device="cuda"), topk_w=torch.empty((0, k), device="cuda")) \
-        if given else dict(logits=torch.empty((0, E), device="cuda"))
+    pairs = dict(topk_idx=torch.empty((0, k), dtype=torch.int32, device="cuda"), topk_w=torch.empty((0, k), device="cuda"))
+    kw = pairs if given else dict(logits=torch.empty((0, E), device="cuda"))
     out, idx, wt = tre.moe_forward_fp8(x, *w, k, **kw) if form == "layer8" else few_call(tre, form, x, w, k, **kw)
     sync()
     assert out.shape == (0, d) and idx.shape == (0, k) and wt.shape == (0, k)
+
+
+# ---- the widest layers and the most experts -----------------------------------------------------------
+
+WIDE, PIECE = (1 << 22) - 64, 1 << 19
+
+
+def long_times(a, q):
+    """a [n, K] @ codes [N, K] transposed in 64 bits, in pieces of either side."""
+    out = T().zeros((a.shape[0], q.shape[0]), dtype=T().float64, device="cuda")
+    for n in range(0, q.shape[0], PIECE):
+        rows = q[n:n + PIECE]
+        for k in range(0, a.shape[1], PIECE):
+            part = rows[:, k:k + PIECE].float().double()
+            out[:, n:n + PIECE] += a[:, k:k + PIECE].double() @ part.t().contiguous()
+    return out
+
+
+@pytest.mark.parametrize("d,I", [(WIDE, 64), (64, WIDE)])
+def test_widest_layers(tre, d, I):
+    """Widths next to 2^22.  Codes are +-0.5 and +-1 and every scale 1, so block sums are exact, and so is their sum
+    while it stays below 2^22, which random signs see to (checked)."""
+    torch = T()
+    g = torch.Generator(device="cuda").manual_seed(d)
+
+    def codes(*shape):
+        q = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+        return q.bitwise_and_(0x88).bitwise_or_(0x30).view(torch.float8_e4m3fn)
+
+    def product(a, q):
+        pieces = torch.stack([long_times(a[:, k:k + PIECE], q[:, k:k + PIECE]) for k in range(0, a.shape[1], PIECE)])
+        assert float(pieces.cumsum(0).abs().max()) < 2.0 ** 21
+        return pieces.sum(0)
+
+    R, ones = 37, lambda *shape: torch.ones(shape, device="cuda")   # noqa: E731
+    nb, db = ref.blocks(I), ref.blocks(d)
+    gq, dq, xq, aq = codes(1, 2 * I, d), codes(1, d, I), codes(R, d), codes(R, I)
+    offs, shrink = offsets_of([R]), 2.0 ** -11 if d > I else 2.0 ** -4     # gates of ordinary size
+    hq, hs = tre.moe_gate_up_swiglu_fp8(xq, ones(R, db) * shrink, offs, gq, ones(1, 2, nb, db))
+    y = tre.moe_down_proj_fp8(aq, ones(R, nb), offs, dq, ones(1, db, nb))
+    rows = torch.tensor([0, 15, 16, 31, 32, 36], device="cuda")
+    pick = lambda q: q.view(torch.uint8)[rows].view(q.dtype).float()       # noqa: E731
+    for n in (0, d - 64) if d > I else (0,):                               # the first and the last columns
+        want = product(pick(aq), dq[0, n:n + 64])
+        assert torch.equal(y[rows, n:n + 64], want.float().to(torch.bfloat16))
+    for n in (0, I - 64) if I > d else (0,):
+        gu = torch.cat([product(pick(xq), gq[0, i * I + n:i * I + n + 64]) for i in (0, 1)], 1) * shrink
+        h, eh = ref.swiglu(gu.cpu().numpy(), np.zeros(gu.shape))
+        # the block's scale comes from all of its 128 columns: only the codes' values are compared here
+        got = hq[rows, n:n + 64].double() * hs[rows, n // 128].double()[:, None]
+        top = hs[rows, n // 128].double().cpu().numpy()[:, None]
+        err = np.abs(got.cpu().numpy() - h)
+        assert np.all(err <= eh + np.maximum(2.0 ** -4 * (np.abs(h) + eh), 2.0 ** -10 * top)), n
+    # the few-token layer, two tokens
+    x = torch.randn((2, d), device="cuda", generator=g).mul(0.5 * shrink).to(torch.bfloat16)
+    idx, wt = to_device(np.zeros((2, 1), np.int32)), ones(2, 1)
+    out, _, _ = tre.moe_forward_few_fp8(x, gq, ones(1, 2, nb, db), dq, ones(1, db, nb), 1, topk_idx=idx, topk_w=wt)
+    gate, up = long_times(x, gq[0]).chunk(2, 1)
+    want = long_times(gate / (1 + torch.exp(-gate)) * up, dq[0])
+    err = float((out.double() - want).norm() / want.norm())
+    # h and the output are rounded to bf16 (independent errors: a half step each in the norm); float32 sums of 2^22
+    # terms of random signs add 2^11 steps of 2^-24 to either product
+    assert err <= 2 * ref.HALF_BF16 + 2 * 2.0 ** -13, err
+
+
+@pytest.mark.parametrize("E", [65, 129, 256])
+def test_many_experts(tre, E):
+    """Groups over all four waves of experts: rows in the first, the last and every third one, exactly."""
+    torch = T()
+    counts = [(e % 5) * 9 if e % 3 == 0 or e == E - 1 else 0 for e in range(E)]
+    counts[0], counts[-1] = 40, 33
+    R, K, N = sum(counts), 192, 128
+    g = torch.Generator(device="cuda").manual_seed(E)
+
+    def codes(*shape):
+        q = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+        return q.bitwise_and_(0x88).bitwise_or_(0x30).view(torch.float8_e4m3fn)
+
+    aq, as_ = codes(R, K), torch.ones((R, 2), device="cuda")
+    w, ws = codes(E, N, K), torch.ones((E, 1, 2), device="cuda")
+    y = tre.moe_down_proj_fp8(aq, as_, offsets_of(counts), w, ws)
+    at = 0
+    for e, n in enumerate(counts):
+        want = aq[at:at + n].float().double() @ w[e].float().double().t().contiguous()
+        assert torch.equal(y[at:at + n], want.float().to(torch.bfloat16)), e
+        at += n
