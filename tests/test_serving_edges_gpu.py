@@ -1,7 +1,8 @@
 """The serving operators on the GPU at the ends of their ranges: gates whose
 SwiGLU factors leave float32 though the product does not, layers whose weights
 pass 2^31 bytes, the widest layers and the most experts, the same rows in calls
-of different sizes, and what the binding takes and refuses."""
+of different sizes, the steps captured, on side streams and with offsets out of
+range, and what the binding takes and refuses."""
 import numpy as np
 import pytest
 
@@ -180,6 +181,117 @@ def test_rows_alone_and_among_others(tre):
         tol = product_tolerance(want, bound)
         for y in (y1, y2):
             assert np.all(np.abs(y[r].double().cpu().numpy() - want) <= tol), e
+
+
+# ---- each step by itself: captured, on a side stream, in its own rows only -------------------------------
+
+def steps(tre, seed):
+    """Calls of the operators that the layers are made of, each (call, its outputs, what it reads and may change)."""
+    torch = T()
+    E, d, I, R = 4, 192, 320, 90
+    w, _, _ = weights8(E, d, I, seed)
+    wb = rand((E, d, 2 * I), "bf16", seed, 0.05)[0], rand((E, I, d), "bf16", seed + 1, 0.05)[0]
+    x, offs = rand((R, d), "bf16", seed + 2)[0], offsets_of([30, 0, 41, 19])
+    xq, xs = random_codes((R, d), seed + 3), random_scales((R, ref.blocks(d)), seed + 4, 0.002, 0.02)
+    aq, as_ = random_codes((R, I), seed + 5), random_scales((R, ref.blocks(I)), seed + 6, 0.01, 0.02)
+    f8 = lambda *n: torch.full(n, 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)   # noqa: E731
+    f32 = lambda *n: torch.full(n, float("nan"), device="cuda")                                       # noqa: E731
+    y = [torch.full((R, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ws = torch.full((tre.load().moe_grouped_ffn_fp8_workspace_size(R, I),), 0xFF, dtype=torch.uint8, device="cuda")
+    q, h = (f8(R, d), f32(R, ref.blocks(d))), (f8(R, I), f32(R, ref.blocks(I)))
+    return {
+        "rows": (lambda st=None: tre.moe_quantize_rows(x, q=q[0], scale=q[1], stream=st), q, x),
+        "weights": (lambda st=None: tre.moe_quantize_weights(*wb, stream=st), None, wb[0]),
+        "gate_up": (lambda st=None: tre.moe_gate_up_swiglu_fp8(xq, xs, offs, *w[:2], h_q=h[0], h_s=h[1], stream=st), h, xs),
+        "down": (lambda st=None: tre.moe_down_proj_fp8(aq, as_, offs, *w[2:], y_perm=y[0], stream=st), y[:1], as_),
+        "ffn": (lambda st=None: tre.moe_grouped_ffn_fp8(xq, xs, offs, *w, y_perm=y[1], workspace=ws, stream=st), y[1:], xs),
+    }
+
+
+def bits(out):
+    return [t.view(T().uint8).clone() for t in (out if isinstance(out, (tuple, list)) else [out])]
+
+
+STEPS = ["rows", "weights", "gate_up", "down", "ffn"]
+
+
+@pytest.mark.parametrize("step", STEPS)
+def test_steps_replayed(tre, step):
+    """Captured once, replayed on changing inputs: the eager call's bits each time."""
+    torch = T()
+    call, out, source = steps(tre, 230)[step]
+    call()
+    sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call()                      # (the weights' outputs belong to the graph)
+    for r in range(4):
+        source.mul_(0.75 if r % 2 else 1.5)
+        g.replay()
+        replayed = bits(got)
+        for t in out or ():
+            t.view(torch.uint8).fill_(0x7F)
+        eager = bits(call())
+        sync()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, eager)), r
+
+
+@pytest.mark.parametrize("step", STEPS)
+def test_steps_on_side_streams(tre, step):
+    """Two streams at once, each with its own inputs: the bits of the calls by themselves."""
+    torch = T()
+    pairs = [steps(tre, 240 + 20 * i)[step][0] for i in range(2)]
+    want = [bits(call()) for call in pairs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sync()
+    for _ in range(5):
+        got = [call(st) for call, st in zip(pairs, streams)]
+        sync()
+        for o, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(bits(o), w))
+
+
+@pytest.mark.parametrize("counts", [[30, 0, 3], [300, 0, 140]])
+def test_gate_up_leaves_other_rows(tre, counts):
+    """Rows of codes and scales behind the last expert's stay as they were."""
+    torch = T()
+    d, I, R, spare = 128, 320, sum(counts), 70
+    w, _, _ = weights8(3, d, I, 250)
+    xq, xs = random_codes((R + spare, d), 251), random_scales((R + spare, 1), 252, 0.002, 0.02)
+    hq = torch.full((R + spare, I), 0x55, dtype=torch.uint8, device="cuda")
+    hs = torch.full((R + spare, ref.blocks(I)), -3.0, device="cuda")
+    tre.moe_gate_up_swiglu_fp8(xq, xs, offsets_of(counts), *w[:2], h_q=hq.view(torch.float8_e4m3fn), h_s=hs)
+    sync()
+    assert torch.all(hq[R:] == 0x55) and torch.all(hs[R:] == -3.0) and torch.all(hs[:R] > 0)
+
+
+@pytest.mark.parametrize("offsets", [[0, -5, 60, 40], [70, 10, 1 << 30, 64], [-9, -8, -7, -6], [64, 3, 2, 1]])
+def test_offsets_out_of_range(tre, offsets):
+    """Offsets that fall, or leave [0, max_rows], are taken back into it: nothing outside the outputs is written, and
+    an expert whose own two offsets are in order gets its product."""
+    torch = T()
+    d, I, R = 192, 128, 64
+    w, _, wd = weights8(3, d, I, 260)
+    aq, as_ = random_codes((R, I), 261), random_scales((R, 1), 262, 0.01, 0.02)
+    xq, xs = random_codes((R, d), 263), random_scales((R, 2), 264, 0.002, 0.02)
+    y = torch.full((3 * R, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    hq, hs = torch.full((3 * R, I), 0x55, dtype=torch.uint8, device="cuda"), torch.full((3 * R, 1), -3.0, device="cuda")
+    offs = to_device(np.array(offsets, np.int32))
+    tre.moe_down_proj_fp8(aq, as_, offs, *w[2:], y_perm=y[R:2 * R])
+    tre.moe_gate_up_swiglu_fp8(xq, xs, offs, *w[:2], h_q=hq[R:2 * R].view(torch.float8_e4m3fn), h_s=hs[R:2 * R])
+    sync()
+    for t, v in ((y, 7.0), (hq, 0x55), (hs, -3.0)):
+        assert torch.all(t[:R] == v) and torch.all(t[2 * R:] == v)
+    clip = np.clip(offsets, 0, R)
+    owners = [[e for e in range(3) if clip[e] <= r < clip[e + 1]] for r in range(R)]
+    a = ref.row_values(aq, as_)
+    for r in range(R):
+        if len(owners[r]) == 1:
+            want, bound = ref.product(a[r:r + 1], wd[owners[r][0]], 3, codes8=True)
+            err = np.abs(y[R + r].double().cpu().numpy() - want[0])
+            assert np.all(err <= product_tolerance(want, bound)[0]), r
+        elif not owners[r]:
+            assert torch.all(y[R + r] == 7.0), r
 
 
 # ---- the binding ------------------------------------------------------------------------------------
