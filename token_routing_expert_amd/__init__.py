@@ -19,9 +19,14 @@ and, from include/moe_serving.h:
   moe_gate_up_swiglu_fp8 / moe_down_proj_fp8 / moe_grouped_ffn_fp8   the grouped products on them
   moe_forward_fp8   the whole layer on 8-bit expert weights
   moe_forward_few / moe_forward_few_fp8   the whole layer for a few tokens, in two kernels
+and, from include/moe_training.h:
+  moe_grouped_ffn_train / moe_grouped_ffn_backward   the grouped feed-forward of a training step and its gradients
+  moe_forward_train_q8 / moe_backward_q8   the whole layer's, with the pre-activations kept in 8 bits in between
+  moe_checkpoint_values   the pre-activations that such a checkpoint stands for
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import re
@@ -31,6 +36,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmoe.so")
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmoe_debug.so")   # the same entry points, device checks compiled in
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "moe.h")
 SERVING_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "moe_serving.h")
+TRAINING_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "moe_training.h")
 
 MOE_F32 = 0
 MOE_BF16 = 1
@@ -90,6 +96,15 @@ def open_library(path: str):
         "moe_forward_few": ([p, p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, sz, p], st),
         "moe_forward_few_fp8_workspace_size": ([i32, i32, i32, i32, i32], sz),
         "moe_forward_few_fp8": ([p, p, i32, i32, i32, i32, i32, p, p, p, p, p, p, p, p, sz, p], st),
+        "moe_grouped_ffn_train_workspace_size": ([i32, i32, i32, i32, st], sz),
+        "moe_grouped_ffn_train": ([p, p, i32, i32, i32, i32, p, p, st, p, p, p, p, sz, p], st),
+        "moe_grouped_ffn_backward_workspace_size": ([i32, i32, i32, i32, st], sz),
+        "moe_grouped_ffn_backward": ([p, p, i32, i32, i32, i32, p, p, st, p, p, p, p, p, p, p, sz, p], st),
+        "moe_forward_train_q8_workspace_size": ([i32, i32, i32, i32, i32, st], sz),
+        "moe_forward_train_q8": ([p, p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, p, p, p, p, p, sz, p], st),
+        "moe_backward_q8_workspace_size": ([i32, i32, i32, i32, i32, st], sz),
+        "moe_backward_q8": ([p, i32, i32, i32, i32, i32, p, p, st, p, p, p, p, p, p, p, p, p, p, p, p, p, p, sz, p], st),
+        "moe_checkpoint_values": ([p, p, i32, i32, st, p, p], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -515,7 +530,7 @@ def moe_backward(x, w_gate_up, w_down, k: int, dout, logits=None, topk_idx=None,
 
 # ---- serving entry points (include/moe_serving.h) -----------------------------------
 #
-# Tensors of one call live on one GPU, which need not be the current one; what
+# (These and the training entry points.)  Tensors of one call live on one GPU, which need not be the current one; what
 # a call allocates itself belongs to the stream it runs on.
 
 FEW_MAX_TOKENS = 64
@@ -799,3 +814,182 @@ def moe_forward_few_fp8(x, w_gate_up_q, w_gate_up_s, w_down_q, w_down_s, k: int,
     c.run("moe_forward_few_fp8", lib.moe_forward_few_fp8, px, plg, T, d, E, k, I, *pws, pi, pw,
           c.tensor(out, torch.bfloat16, (T, d), "out"), pwork, nbytes)
     return out, topk_idx, topk_w
+
+
+# ---- training entry points (include/moe_training.h) -----------------------------------
+
+KEEP_BLOCK = 64   # columns of a checkpoint that share a scale
+
+# What moe_forward_train_q8 keeps for moe_backward_q8: the grouping (expert_offsets [E+1], row_token [T*k], pair_row
+# [T*k], int32) and the grouped rows' pre-activations (gu_q [T*k, 2I] int8, gu_s [T*k, 2, I/64] float32).
+Checkpoint = collections.namedtuple("Checkpoint", "expert_offsets row_token pair_row gu_q gu_s")
+
+
+def _ffn_weights(c, w_gate_up, w_down, dtype, d):
+    """(E, I, addresses of the two weight tensors)."""
+    E, d2, two_i = w_gate_up.shape
+    I = two_i // 2
+    if d2 != d or two_i != 2 * I:
+        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} does not match d={d}")
+    return E, I, (c.tensor(w_gate_up, dtype, (E, d, 2 * I), "w_gate_up"), c.tensor(w_down, dtype, (E, I, d), "w_down"))
+
+
+def _checkpoint_blocks(I: int) -> int:
+    """Blocks of a row's half; a width that the library refuses gets a shape that it never reads."""
+    return -(-I // KEEP_BLOCK)
+
+
+def moe_grouped_ffn_train_workspace_size(max_rows: int, E: int, d: int, I: int, dtype) -> int:
+    return int(load().moe_grouped_ffn_train_workspace_size(max_rows, E, d, I, dtype))
+
+
+def moe_grouped_ffn_train(x_perm, expert_offsets, w_gate_up, w_down, y_perm=None, gu_q=None, gu_s=None,
+                          workspace=None, stream=None):
+    """moe_grouped_ffn for a training step: x_perm [R, d] rows grouped by expert_offsets [E+1] ->
+    (y_perm [R, d], gu_q [R, 2I] int8, gu_s [R, 2, I/64] float32); y_perm as moe_grouped_ffn computes it, and the
+    8-bit checkpoint of the rows' pre-activations for moe_grouped_ffn_backward."""
+    torch = _torch()
+    lib = load()
+    R, d = x_perm.shape
+    dt = _dt(x_perm)
+    c = _Call(x_perm, stream)
+    px = c.tensor(x_perm, x_perm.dtype, (R, d), "x_perm")
+    E, I, pws = _ffn_weights(c, w_gate_up, w_down, x_perm.dtype, d)
+    po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    nb = _checkpoint_blocks(I)
+    y_perm = c.empty((R, d), x_perm.dtype) if y_perm is None else y_perm
+    gu_q = c.empty((R, 2 * I), torch.int8) if gu_q is None else gu_q
+    gu_s = c.empty((R, 2, nb), torch.float32) if gu_s is None else gu_s
+    nbytes = lib.moe_grouped_ffn_train_workspace_size(R, E, d, I, dt)
+    ws, pwork = c.workspace(workspace, nbytes)
+    c.run("moe_grouped_ffn_train", lib.moe_grouped_ffn_train, px, po, R, E, d, I, *pws, dt,
+          c.tensor(y_perm, x_perm.dtype, (R, d), "y_perm"), c.tensor(gu_q, torch.int8, (R, 2 * I), "gu_q"),
+          c.tensor(gu_s, torch.float32, (R, 2, nb), "gu_s"), pwork, nbytes)
+    return y_perm, gu_q, gu_s
+
+
+def moe_grouped_ffn_backward_workspace_size(max_rows: int, E: int, d: int, I: int, dtype) -> int:
+    return int(load().moe_grouped_ffn_backward_workspace_size(max_rows, E, d, I, dtype))
+
+
+def moe_grouped_ffn_backward(x_perm, expert_offsets, w_gate_up, w_down, dy_perm, gu_q=None, gu_s=None, dx_perm=None,
+                             dw_gate_up=None, dw_down=None, workspace=None, stream=None):
+    """Gradients of <dy_perm, moe_grouped_ffn(x_perm, ...)> -> (dx_perm [R, d], dw_gate_up [E, d, 2I],
+    dw_down [E, I, d]).  With ``gu_q`` and ``gu_s`` (moe_grouped_ffn_train's) the pre-activations come from the
+    checkpoint; without, they are computed again from x_perm."""
+    torch = _torch()
+    lib = load()
+    R, d = x_perm.shape
+    dtype, dt = x_perm.dtype, _dt(x_perm)
+    c = _Call(x_perm, stream)
+    px, pdy = c.tensor(x_perm, dtype, (R, d), "x_perm"), c.tensor(dy_perm, dtype, (R, d), "dy_perm")
+    E, I, pws = _ffn_weights(c, w_gate_up, w_down, dtype, d)
+    po = c.tensor(expert_offsets, torch.int32, (E + 1,), "expert_offsets")
+    if (gu_q is None) != (gu_s is None):
+        raise ValueError("gu_q and gu_s belong together")
+    pq = ps = None
+    if gu_q is not None:
+        pq = c.tensor(gu_q, torch.int8, (R, 2 * I), "gu_q")
+        ps = c.tensor(gu_s, torch.float32, (R, 2, _checkpoint_blocks(I)), "gu_s")
+    dx_perm = c.empty((R, d), dtype) if dx_perm is None else dx_perm
+    dw_gate_up = c.empty((E, d, 2 * I), dtype) if dw_gate_up is None else dw_gate_up
+    dw_down = c.empty((E, I, d), dtype) if dw_down is None else dw_down
+    nbytes = lib.moe_grouped_ffn_backward_workspace_size(R, E, d, I, dt)
+    ws, pwork = c.workspace(workspace, nbytes)
+    c.run("moe_grouped_ffn_backward", lib.moe_grouped_ffn_backward, px, po, R, E, d, I, *pws, dt, pq, ps, pdy,
+          c.tensor(dx_perm, dtype, (R, d), "dx_perm"), c.tensor(dw_gate_up, dtype, (E, d, 2 * I), "dw_gate_up"),
+          c.tensor(dw_down, dtype, (E, I, d), "dw_down"), pwork, nbytes)
+    return dx_perm, dw_gate_up, dw_down
+
+
+def moe_forward_train_q8_workspace_size(T: int, d: int, E: int, k: int, I: int, dtype) -> int:
+    return int(load().moe_forward_train_q8_workspace_size(T, d, E, k, I, dtype))
+
+
+def moe_forward_train_q8(x, w_gate_up, w_down, k: int, logits=None, topk_idx=None, topk_w=None, out=None, kept=None,
+                         workspace=None, stream=None):
+    """The forward of a training step: ``out`` as moe_forward computes it, and what the backward needs in a
+    Checkpoint (``kept``: one to fill again, new tensors when None).  The workspace is free again when the call's
+    work has run.  Returns (out [T, d], topk_idx, topk_w, Checkpoint)."""
+    torch = _torch()
+    lib = load()
+    T, d = x.shape
+    dtype, dt = x.dtype, _dt(x)
+    c = _Call(x, stream)
+    px = c.tensor(x, dtype, (T, d), "x")
+    E, I, pws = _ffn_weights(c, w_gate_up, w_down, dtype, d)
+    plg, topk_idx, topk_w, pi, pw = _routing(c, logits, topk_idx, topk_w, T, E, k)
+    out = c.empty((T, d), dtype) if out is None else out
+    if kept is None:
+        i32 = torch.int32
+        kept = Checkpoint(c.empty((E + 1,), i32), c.empty((T * k,), i32), c.empty((T * k,), i32),
+                          c.empty((T * k, 2 * I), torch.int8),
+                          c.empty((T * k, 2, _checkpoint_blocks(I)), torch.float32))
+    nbytes = lib.moe_forward_train_q8_workspace_size(T, d, E, k, I, dt)
+    ws, pwork = c.workspace(workspace, nbytes)
+    c.run("moe_forward_train_q8", lib.moe_forward_train_q8, px, plg, T, d, E, k, I, *pws, dt, pi, pw,
+          *_kept_tensors(c, kept, T, E, k, I), c.tensor(out, dtype, (T, d), "out"), pwork, nbytes)
+    return out, topk_idx, topk_w, kept
+
+
+def _kept_tensors(c, kept, T, E, k, I):
+    """Addresses of a Checkpoint's tensors."""
+    torch = _torch()
+    return (c.tensor(kept.expert_offsets, torch.int32, (E + 1,), "expert_offsets"),
+            c.tensor(kept.row_token, torch.int32, (T * k,), "row_token"),
+            c.tensor(kept.pair_row, torch.int32, (T * k,), "pair_row"),
+            c.tensor(kept.gu_q, torch.int8, (T * k, 2 * I), "gu_q"),
+            c.tensor(kept.gu_s, torch.float32, (T * k, 2, _checkpoint_blocks(I)), "gu_s"))
+
+
+def moe_backward_q8_workspace_size(T: int, d: int, E: int, k: int, I: int, dtype) -> int:
+    return int(load().moe_backward_q8_workspace_size(T, d, E, k, I, dtype))
+
+
+def moe_backward_q8(x, w_gate_up, w_down, k: int, dout, topk_idx, topk_w, kept, want_dlogits: bool = False, dx=None,
+                    dw_gate_up=None, dw_down=None, workspace=None, stream=None):
+    """Gradients of <dout, moe_forward_train_q8(x, ...)> from its Checkpoint ``kept`` and its topk_idx / topk_w.
+    ``want_dlogits``: the logits' gradient too, for pairs that were routed by logits.
+    Returns a dict with dx, dw_gate_up, dw_down, dtopk_w and (if wanted) dlogits."""
+    torch = _torch()
+    lib = load()
+    T, d = x.shape
+    dtype, dt = x.dtype, _dt(x)
+    c = _Call(x, stream)
+    px, pdo = c.tensor(x, dtype, (T, d), "x"), c.tensor(dout, dtype, (T, d), "dout")
+    E, I, pws = _ffn_weights(c, w_gate_up, w_down, dtype, d)
+    _, _, _, pi, pw = _routing(c, None, topk_idx, topk_w, T, E, k)
+    pk = _kept_tensors(c, kept, T, E, k, I)
+    dx = c.empty((T, d), dtype) if dx is None else dx
+    dw_gate_up = c.empty((E, d, 2 * I), dtype) if dw_gate_up is None else dw_gate_up
+    dw_down = c.empty((E, I, d), dtype) if dw_down is None else dw_down
+    dtopk_w = c.empty((T, k), torch.float32)
+    dlogits = c.empty((T, E), torch.float32) if want_dlogits else None
+    nbytes = lib.moe_backward_q8_workspace_size(T, d, E, k, I, dt)
+    ws, pwork = c.workspace(workspace, nbytes)
+    c.run("moe_backward_q8", lib.moe_backward_q8, px, T, d, E, k, I, *pws, dt, pi, pw, *pk, pdo,
+          c.tensor(dx, dtype, (T, d), "dx"), c.tensor(dw_gate_up, dtype, (E, d, 2 * I), "dw_gate_up"),
+          c.tensor(dw_down, dtype, (E, I, d), "dw_down"), dtopk_w.data_ptr(),
+          None if dlogits is None else dlogits.data_ptr(), pwork, nbytes)
+    res = dict(dx=dx, dw_gate_up=dw_gate_up, dw_down=dw_down, dtopk_w=dtopk_w)
+    if dlogits is not None:
+        res["dlogits"] = dlogits
+    return res
+
+
+def moe_checkpoint_values(gu_q, gu_s, dtype, gu=None, stream=None):
+    """The pre-activations that an 8-bit checkpoint stands for: gu_q [R, 2I], gu_s [R, 2, I/64] -> gu [R, 2I] in
+    ``dtype`` (torch.float32 or torch.bfloat16), gate columns first."""
+    torch = _torch()
+    lib = load()
+    R, two_i = gu_q.shape
+    I = two_i // 2
+    if two_i != 2 * I:
+        raise ValueError(f"gu_q {tuple(gu_q.shape)}: the last dimension is 2I")
+    c = _Call(gu_q, stream)
+    pq = c.tensor(gu_q, torch.int8, (R, two_i), "gu_q")
+    ps = c.tensor(gu_s, torch.float32, (R, 2, _checkpoint_blocks(I)), "gu_s")
+    gu = c.empty((R, two_i), dtype) if gu is None else gu
+    c.run("moe_checkpoint_values", lib.moe_checkpoint_values, pq, ps, R, I, _dt(gu),
+          c.tensor(gu, dtype, (R, two_i), "gu"))
+    return gu

@@ -1,0 +1,335 @@
+// api_training.hip -- the C ABI of include/moe_training.h: host-side
+// validation, workspace carving and kernel launches.  Every argument is checked
+// before anything is enqueued; no call allocates, frees or synchronises.
+#include "../../include/moe_training.h"
+#include "checks.hpp"
+
+using namespace tre;
+
+namespace {
+
+// Whether every address is a multiple of 16 (a NULL that reaches here is a
+// missing workspace).
+template <typename... P>
+bool aligned16(const P*... p) {
+  return ((((uintptr_t)p & 15) == 0) && ...);
+}
+
+// A tile's 256 rows of [dg | du] are addressed with 31 bits.
+constexpr int32_t kMaxWidth = 1 << 21;
+
+moe_status check_sizes(moe_dtype dt, int32_t E, int32_t d, int32_t I) {
+  if (!dtype_ok(dt)) return MOE_ERR_ARG;
+  TRY(check_experts(E));
+  TRY(check_width(d));
+  TRY(check_width(I));
+  if (d >= kMaxWidth || I >= kMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)E * d * 2 * I >= 8 * kMaxElems) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)d * I * 4 >= kMaxElems) return MOE_ERR_UNSUPPORTED;   // one expert's weights < 2 GiB
+  return MOE_OK;
+}
+
+moe_status check_rows(moe_dtype dt, int64_t rows, int32_t E, int32_t d, int32_t I) {
+  if (rows < 0) return MOE_ERR_ARG;
+  TRY(check_sizes(dt, E, d, I));
+  if (rows * (d > 2 * (int64_t)I ? d : 2 * (int64_t)I) >= kMaxElems) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_layer(moe_dtype dt, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I) {
+  if (T < 0 || k < 1) return MOE_ERR_ARG;
+  TRY(check_rows(dt, (int64_t)T * k, E, d, I));
+  if ((int64_t)T * E >= kMaxElems) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)T * d >= kMaxElems / 2) return MOE_ERR_UNSUPPORTED;   // token rows are addressed with 32-bit byte offsets
+  return MOE_OK;
+}
+
+bool sizes_positive(int64_t rows, int32_t d, int32_t E, int32_t I, moe_dtype dt) {
+  return rows >= 0 && d >= 1 && E >= 1 && I >= 1 && dtype_ok(dt);
+}
+
+// What the two products of a forward use beside their operands: h, float32's
+// pre-activations before they are rounded, and (bf16) the down projection's
+// partial sums and the products' tile counters.
+struct FfnLayout {
+  size_t h, gu, split, sched, total;
+};
+
+FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt) {
+  FfnLayout L;
+  size_t o = 0;
+  L.h = o;     o += align256((size_t)(rows * I) * elem_size(dt));
+  L.gu = o;    o += dt == MOE_F32 ? align256((size_t)(rows * 2 * I) * 4) : 0;
+  L.split = o; o += dt == MOE_BF16 ? align256(split_workspace(rows, (int)E, (int)d, (int)I)) : 0;
+  L.sched = o; o += dt == MOE_BF16 ? align256(kSchedWords * 4) : 0;
+  L.total = o;
+  return L;
+}
+
+struct LayerLayout {
+  size_t perm_ws, row_w, x_perm, y, ffn, total;
+};
+
+LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, moe_dtype dt) {
+  const int64_t P = T * k;
+  LayerLayout L;
+  size_t o = 0;
+  L.perm_ws = o; o += permute_index_workspace(P, (int)E);
+  L.row_w = o;   o += dt == MOE_BF16 && k == 1 ? align256((size_t)P * 4) : 0;
+  L.x_perm = o;  o += dt == MOE_F32 ? align256((size_t)(P * d) * 4) : 0;   // bf16 gathers rows in place
+  L.y = o;       o += align256((size_t)(P * d) * elem_size(dt));
+  L.ffn = o;     o += ffn_layout(P, d, E, I, dt).total;
+  L.total = o;
+  return L;
+}
+
+// The gradients of grouped rows: h and dgu (times the rows' weights), g | u
+// where they are computed again (float32, or bf16's 16-bit codes and their
+// scales), float32's dh.
+struct GradLayout {
+  size_t h, dgu, gu, gu_s, dh, total;
+};
+
+GradLayout grad_layout(int64_t rows, int64_t I, moe_dtype dt, bool again) {
+  const size_t s = elem_size(dt);
+  GradLayout L;
+  size_t o = 0;
+  L.h = o;   o += align256((size_t)(rows * I) * s);
+  L.dgu = o; o += align256((size_t)(rows * 2 * I) * s);
+  L.gu = o;  o += again ? align256((size_t)(rows * 2 * I) * s) : 0;
+  L.gu_s = o; o += again && dt == MOE_BF16 ? align256((size_t)(rows * 2 * (I / kKeepBlock)) * 4) : 0;
+  L.dh = o;  o += dt == MOE_F32 ? align256((size_t)(rows * I) * 4) : 0;
+  L.total = o;
+  return L;
+}
+
+// The layer's backward around them: the grouped rows of x and dout, their
+// weights, the dot products' parts, and the rows' dx.
+struct BackwardLayout {
+  size_t x_perm, dout_perm, row_w, dot, dx_perm, grad, total;
+};
+
+int64_t dot_columns(int64_t I, moe_dtype dt) { return dt == MOE_F32 ? 1 : dot_parts((int)I); }
+
+BackwardLayout backward_layout(int64_t T, int64_t d, int64_t k, int64_t I, moe_dtype dt) {
+  const int64_t P = T * k;
+  const size_t s = elem_size(dt);
+  BackwardLayout L;
+  size_t o = 0;
+  L.x_perm = o;    o += align256((size_t)(P * d) * s);
+  L.dout_perm = o; o += align256((size_t)(P * d) * s);
+  L.row_w = o;     o += align256((size_t)P * 4);
+  L.dot = o;       o += align256((size_t)(P * dot_columns(I, dt)) * 4);
+  L.dx_perm = o;   o += align256((size_t)(P * d) * s);
+  L.grad = o;      o += grad_layout(P, I, dt, false).total;
+  L.total = o;
+  return L;
+}
+
+moe_status zero_weight_gradients(int32_t E, int32_t d, int32_t I, moe_dtype dt, void* dw_gate_up, void* dw_down,
+                                 hipStream_t s) {
+  if (!dw_gate_up || !dw_down || !aligned16(dw_gate_up, dw_down)) return MOE_ERR_ARG;
+  const int64_t halves = dt == MOE_F32 ? 2 : 1;   // a float32 element is cleared as two bf16 ones
+  TRY(from_hip(launch_zero_bf16((bf16_t*)dw_gate_up, (int64_t)E * d * 2 * I * halves, s)));
+  return from_hip(launch_zero_bf16((bf16_t*)dw_down, (int64_t)E * I * d * halves, s));
+}
+
+// The gradients of grouped rows x with dy (times row_w): from the checkpoint,
+// or, where kept.q is null, from g | u computed again.  dot: see launch_down_bwd_bf16.
+moe_status grad_rows(const void* x, const void* dy, const float* row_w, const int32_t* offs, int64_t rows, int32_t E,
+                     int32_t d, int32_t I, const void* w_gate_up, const void* w_down, moe_dtype dt, const Kept& kept,
+                     void* dx, void* dw_gate_up, void* dw_down, float* dot, char* ws, const GradLayout& L,
+                     hipStream_t s) {
+  const bool again = kept.q == nullptr;
+  if (dt == MOE_F32) {
+    const float *fx = (const float*)x, *fdy = (const float*)dy, *fwgu = (const float*)w_gate_up,
+                *fwd = (const float*)w_down;
+    float *h = (float*)(ws + L.h), *dgu = (float*)(ws + L.dgu), *gu = (float*)(ws + L.gu), *dh = (float*)(ws + L.dh);
+    if (again) TRY(from_hip(launch_gate_up_save_f32(fx, offs, rows, E, d, I, fwgu, h, gu, s)));
+    TRY(from_hip(launch_down_dgrad_f32(fdy, offs, rows, E, d, I, fwd, dh, s)));
+    TRY(from_hip(launch_swiglu_bwd_f32(dh, again ? gu : nullptr, kept, row_w, offs, E, rows, I, dgu, h, dot, s)));
+    TRY(from_hip(launch_wgrad_f32(h, I, I, fdy, d, d, offs, rows, E, (float*)dw_down, s)));
+    TRY(from_hip(launch_gate_up_dgrad_f32(dgu, offs, rows, E, d, I, fwgu, (float*)dx, s)));
+    return from_hip(launch_wgrad_f32(fx, d, d, dgu, 2 * I, 2 * I, offs, rows, E, (float*)dw_gate_up, s));
+  }
+  const bf16_t *bx = (const bf16_t*)x, *bdy = (const bf16_t*)dy, *wgu = (const bf16_t*)w_gate_up,
+               *wd = (const bf16_t*)w_down;
+  bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
+  const Kept own{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s)};
+  if (again) TRY(from_hip(launch_gate_up_keep16_bf16(bx, offs, rows, E, d, I, wgu, own, s, nullptr)));
+  TRY(from_hip(launch_down_bwd_bf16(bdy, offs, rows, E, d, I, wd, again ? own : kept, again ? 16 : 8, row_w, dgu, h,
+                                    dot, s, nullptr, 0)));
+  TRY(from_hip(launch_wgrad_bf16(h, I, I, bdy, d, d, offs, rows, E, (bf16_t*)dw_down, s)));
+  TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, offs, rows, E, d, I, wgu, (bf16_t*)dx, s)));
+  return from_hip(launch_wgrad_bf16(bx, d, d, dgu, 2 * I, 2 * I, offs, rows, E, (bf16_t*)dw_gate_up, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grouped_ffn_train_workspace_size(int32_t max_rows, int32_t E, int32_t d, int32_t I, moe_dtype dt) {
+  if (!sizes_positive(max_rows, d, E, I, dt)) return 0;
+  return ffn_layout(max_rows, d, E, I, dt).total;
+}
+
+moe_status moe_grouped_ffn_train(const void* x_perm, const int32_t* expert_offsets, int32_t max_rows, int32_t E,
+                                 int32_t d, int32_t I, const void* w_gate_up, const void* w_down, moe_dtype dt,
+                                 void* y_perm, void* gu_q, float* gu_s, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  TRY(check_rows(dt, max_rows, E, d, I));
+  if (max_rows == 0) return MOE_OK;
+  if (!x_perm || !expert_offsets || !w_gate_up || !w_down || !y_perm || !gu_q || !gu_s) return MOE_ERR_ARG;
+  if (!aligned16(x_perm, w_gate_up, w_down, y_perm, gu_q, workspace)) return MOE_ERR_ARG;
+  const FfnLayout L = ffn_layout(max_rows, d, E, I, dt);
+  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  char* ws = (char*)workspace;
+  const Kept kept{(int8_t*)gu_q, gu_s};
+  hipStream_t s = (hipStream_t)stream;
+  if (dt == MOE_F32) {
+    float *h = (float*)(ws + L.h), *gu = (float*)(ws + L.gu);
+    TRY(from_hip(launch_gate_up_save_f32((const float*)x_perm, expert_offsets, max_rows, E, d, I,
+                                         (const float*)w_gate_up, h, gu, s)));
+    TRY(from_hip(launch_keep8_f32(gu, expert_offsets, E, max_rows, I, kept, s)));
+    return from_hip(launch_down_f32(h, expert_offsets, max_rows, E, d, I, (const float*)w_down, (float*)y_perm, s));
+  }
+  int32_t* sched = (int32_t*)(ws + L.sched);
+  bf16_t* h = (bf16_t*)(ws + L.h);
+  TRY(from_hip(launch_sched_reset(sched, s)));
+  TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x_perm, expert_offsets, max_rows, E, d, I,
+                                         (const bf16_t*)w_gate_up, h, kept, s, nullptr, 0, sched)));
+  return from_hip(launch_down_bf16(h, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_down, (bf16_t*)y_perm, s,
+                                   (float*)(ws + L.split), sched));
+}
+
+size_t moe_grouped_ffn_backward_workspace_size(int32_t max_rows, int32_t E, int32_t d, int32_t I, moe_dtype dt) {
+  if (!sizes_positive(max_rows, d, E, I, dt)) return 0;
+  return grad_layout(max_rows, I, dt, true).total;
+}
+
+moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_offsets, int32_t max_rows, int32_t E,
+                                    int32_t d, int32_t I, const void* w_gate_up, const void* w_down, moe_dtype dt,
+                                    const void* gu_q, const float* gu_s, const void* dy_perm, void* dx_perm,
+                                    void* dw_gate_up, void* dw_down, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  TRY(check_rows(dt, max_rows, E, d, I));
+  if ((gu_q == nullptr) != (gu_s == nullptr)) return MOE_ERR_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  if (max_rows == 0) return zero_weight_gradients(E, d, I, dt, dw_gate_up, dw_down, s);
+  if (!x_perm || !expert_offsets || !w_gate_up || !w_down || !dy_perm || !dx_perm || !dw_gate_up || !dw_down)
+    return MOE_ERR_ARG;
+  if (!aligned16(x_perm, w_gate_up, w_down, dy_perm, dx_perm, dw_gate_up, dw_down, gu_q, workspace)) return MOE_ERR_ARG;
+  const GradLayout L = grad_layout(max_rows, I, dt, true);
+  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  return grad_rows(x_perm, dy_perm, nullptr, expert_offsets, max_rows, E, d, I, w_gate_up, w_down, dt, kept, dx_perm,
+                   dw_gate_up, dw_down, nullptr, (char*)workspace, L, s);
+}
+
+size_t moe_forward_train_q8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt) {
+  if (!sizes_positive(T, d, E, I, dt) || k < 1) return 0;
+  return layer_layout(T, d, E, k, I, dt).total;
+}
+
+moe_status moe_forward_train_q8(const void* x, const float* logits, int32_t T, int32_t d, int32_t E, int32_t k,
+                                int32_t I, const void* w_gate_up, const void* w_down, moe_dtype dt, int32_t* topk_idx,
+                                float* topk_w, int32_t* expert_offsets, int32_t* row_token, int32_t* pair_row,
+                                void* gu_q, float* gu_s, void* out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  TRY(check_layer(dt, T, d, E, k, I));
+  if (logits && k > E) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_gate_up || !w_down || !topk_idx || !topk_w || !expert_offsets || !row_token || !pair_row || !gu_q ||
+      !gu_s || !out)
+    return MOE_ERR_ARG;
+  if (!aligned16(x, w_gate_up, w_down, gu_q, out, workspace)) return MOE_ERR_ARG;
+  const LayerLayout L = layer_layout(T, d, E, k, I, dt);
+  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const int64_t P = (int64_t)T * k;
+  const FfnLayout F = ffn_layout(P, d, E, I, dt);
+  char *ws = (char*)workspace, *fws = ws + L.ffn;
+  const Kept kept{(int8_t*)gu_q, gu_s};
+  hipStream_t s = (hipStream_t)stream;
+  if (logits) TRY(from_hip(launch_route_topk(logits, T, E, k, topk_idx, topk_w, s)));
+  if (dt == MOE_F32) {
+    float *xp = (float*)(ws + L.x_perm), *h = (float*)(fws + F.h), *gu = (float*)(fws + F.gu), *y = (float*)(ws + L.y);
+    TRY(from_hip(launch_permute_rows(topk_idx, T, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s,
+                                     nullptr, x, (int64_t)d * 4, xp)));
+    TRY(from_hip(launch_gate_up_save_f32(xp, expert_offsets, P, E, d, I, (const float*)w_gate_up, h, gu, s)));
+    TRY(from_hip(launch_keep8_f32(gu, expert_offsets, E, P, I, kept, s)));
+    TRY(from_hip(launch_down_f32(h, expert_offsets, P, E, d, I, (const float*)w_down, y, s)));
+    return from_hip(launch_combine_f32(y, P, pair_row, topk_w, T, k, d, (float*)out, s));
+  }
+  // as moe_forward: rows gathered in the products' loads, and with one pair a
+  // token the down projection writes the output rows itself where its tiles allow
+  int32_t* sched = (int32_t*)(fws + F.sched);
+  bf16_t* h = (bf16_t*)(fws + F.h);
+  float* split = (float*)(fws + F.split);
+  const bool scatter = k == 1 && down_scatters(P, E, d, I, true);
+  float* row_w = scatter ? (float*)(ws + L.row_w) : nullptr;
+  TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s, sched,
+                                    scatter ? topk_w : nullptr, row_w)));
+  if (scatter) TRY(from_hip(launch_zero_unrouted_bf16(pair_row, P, T, d, (bf16_t*)out, s)));
+  TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x, expert_offsets, P, E, d, I, (const bf16_t*)w_gate_up, h,
+                                         kept, s, row_token, T, sched)));
+  if (scatter) {
+    const DownScatter sc{(bf16_t*)out, row_token, row_w, T};
+    return from_hip(launch_down_bf16(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, nullptr, s, split, sched,
+                                     &sc));
+  }
+  bf16_t* y = (bf16_t*)(ws + L.y);
+  TRY(from_hip(launch_down_bf16(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, y, s, split, sched)));
+  return from_hip(launch_combine_bf16(y, P, pair_row, topk_w, T, k, d, (bf16_t*)out, s));
+}
+
+size_t moe_backward_q8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt) {
+  if (!sizes_positive(T, d, E, I, dt) || k < 1) return 0;
+  return backward_layout(T, d, k, I, dt).total;
+}
+
+moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I,
+                           const void* w_gate_up, const void* w_down, moe_dtype dt, const int32_t* topk_idx,
+                           const float* topk_w, const int32_t* expert_offsets, const int32_t* row_token,
+                           const int32_t* pair_row, const void* gu_q, const float* gu_s, const void* dout, void* dx,
+                           void* dw_gate_up, void* dw_down, float* dtopk_w, float* dlogits, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  TRY(check_layer(dt, T, d, E, k, I));
+  if (dlogits && k > E) return MOE_ERR_ARG;
+  hipStream_t s = (hipStream_t)stream;
+  if (T == 0) return zero_weight_gradients(E, d, I, dt, dw_gate_up, dw_down, s);
+  if (!x || !w_gate_up || !w_down || !topk_idx || !topk_w || !expert_offsets || !row_token || !pair_row || !gu_q ||
+      !gu_s || !dout || !dx || !dw_gate_up || !dw_down || !dtopk_w)
+    return MOE_ERR_ARG;
+  if (!aligned16(x, w_gate_up, w_down, gu_q, dout, dx, dw_gate_up, dw_down, workspace)) return MOE_ERR_ARG;
+  const BackwardLayout L = backward_layout(T, d, k, I, dt);
+  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const int64_t P = (int64_t)T * k;
+  char* ws = (char*)workspace;
+  float *row_w = (float*)(ws + L.row_w), *dot = (float*)(ws + L.dot);
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  TRY(from_hip(launch_pair_rows(x, dout, T, k, (int64_t)d * elem_size(dt), pair_row, topk_w, P, ws + L.x_perm,
+                                ws + L.dout_perm, row_w, s)));
+  // the combine's backward puts w_p before dout; it is applied to h and [dg | du] instead, so that dout stays exact
+  const GradLayout G = grad_layout(P, I, dt, false);
+  TRY(grad_rows(ws + L.x_perm, ws + L.dout_perm, row_w, expert_offsets, P, E, d, I, w_gate_up, w_down, dt, kept,
+                ws + L.dx_perm, dw_gate_up, dw_down, dot, ws + L.grad, G, s));
+  TRY(from_hip(launch_pair_grad(dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, E, dtopk_w, dlogits, s)));
+  if (dt == MOE_F32)
+    return from_hip(launch_combine_f32((const float*)(ws + L.dx_perm), P, pair_row, nullptr, T, k, d, (float*)dx, s));
+  return from_hip(launch_combine_bf16((const bf16_t*)(ws + L.dx_perm), P, pair_row, nullptr, T, k, d, (bf16_t*)dx, s));
+}
+
+moe_status moe_checkpoint_values(const void* gu_q, const float* gu_s, int32_t rows, int32_t I, moe_dtype dt, void* gu,
+                                 void* stream) {
+  if (!dtype_ok(dt) || rows < 0) return MOE_ERR_ARG;
+  TRY(check_width(I));
+  if ((int64_t)rows * 2 * I >= kMaxElems) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!gu_q || !gu_s || !gu || !aligned16(gu_q, gu)) return MOE_ERR_ARG;
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  hipStream_t s = (hipStream_t)stream;
+  if (dt == MOE_BF16) return from_hip(launch_keep8_values_bf16(kept, rows, I, (bf16_t*)gu, s));
+  return from_hip(launch_keep8_values_f32(kept, rows, I, (float*)gu, s));
+}
+
+}  // extern "C"

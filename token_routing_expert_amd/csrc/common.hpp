@@ -22,6 +22,9 @@ __device__ __forceinline__ float bf16_to_f32(bf16_t b) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
+// A magnitude as an integer that orders as it does; infinity and NaN are the largest.
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; }
+
 // Round to nearest even (the hardware conversion on gfx950).
 __device__ __forceinline__ bf16_t f32_to_bf16(float f) {
   return __builtin_bit_cast(bf16_t, (__bf16)f);
@@ -308,6 +311,52 @@ hipError_t launch_gate_up_dgrad_f32(const float* dgu, const int32_t* expert_offs
                                     int d, int I, const float* w_gate_up, float* dx_perm, hipStream_t s);
 hipError_t launch_wgrad_f32(const float* a, int lda, int M, const float* b, int ldb, int N,
                             const int32_t* expert_offsets, int64_t max_rows, int E, float* dw, hipStream_t s);
+
+// ---- gradients of the grouped feed-forward, 8-bit checkpoints ----
+// (include/moe_training.h has the checkpoint's format)
+constexpr int kKeepBlock = 64;   // columns that share a scale
+struct Kept {
+  int8_t* q;   // [rows, 2I], of 8 bits (inside a call also of 16)
+  float* s;    // [rows, 2, I/64]
+};
+// gate/up with SwiGLU that also writes the checkpoint of its rows
+hipError_t launch_gate_up_keep8_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                     int I, const bf16_t* w_gate_up, bf16_t* h, const Kept& kept, hipStream_t s,
+                                     const int32_t* row_token, int64_t x_rows, int32_t* sched);
+// the checkpoint in 16-bit codes (q [rows, 2I] int16), alone
+hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                      int I, const bf16_t* w_gate_up, const Kept& kept, hipStream_t s,
+                                      int32_t* sched);
+// dgu = w [dg | du] and h = w silu(g) u from dh = dy Wd^T and a checkpoint of 8 or
+// 16 bits; w = row_w[r], 1 where row_w is null.  With row_token, row r's dy is row
+// row_token[r] of dy [dy_rows, d].  dot (optional, [max_rows, dot_parts(I)]): the
+// parts of <dh, silu(g) u> of each row, one for 128 columns, those past I zero
+int64_t dot_parts(int I);
+hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
+                                bf16_t* h, float* dot, hipStream_t s, const int32_t* row_token, int64_t dy_rows);
+// the checkpoint of gu [rows, 2I] float32 (rows below offsets[E]), and its values
+hipError_t launch_keep8_f32(const float* gu, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
+                            const Kept& kept, hipStream_t s);
+hipError_t launch_keep8_values_f32(const Kept& kept, int64_t rows, int I, float* gu, hipStream_t s);
+hipError_t launch_keep8_values_bf16(const Kept& kept, int64_t rows, int I, bf16_t* gu, hipStream_t s);
+// dgu, h and dot [max_rows] as launch_down_bwd_bf16's from dh [max_rows, I]
+// and g | u (gu, or the checkpoint where gu is null), float32
+hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& kept, const float* row_w,
+                                 const int32_t* expert_offsets, int E, int64_t max_rows, int I, float* dgu, float* h,
+                                 float* dot, hipStream_t s);
+// dh [max_rows, I] = dy Wd^T
+hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 const float* w_down, float* dh, hipStream_t s);
+// each grouped row's token row of x and of dout, and its routing weight
+hipError_t launch_pair_rows(const void* x, const void* dout, int64_t T, int k, int64_t row_bytes,
+                            const int32_t* pair_row, const float* pair_w, int64_t max_rows, void* x_perm,
+                            void* dout_perm, float* row_w, hipStream_t s);
+// dw[p] = the sum of its row's n_parts dot products (0 for a pair without a row); dlogits (optional) as
+// launch_combine_bwd_bf16's
+hipError_t launch_pair_grad(const float* dot, int64_t n_parts, int64_t max_rows, const int32_t* pair_row,
+                            const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int E, float* dw,
+                            float* dlogits, hipStream_t s);
 
 // ---- 8-bit codes and scales (quantize.hip) ----
 // rows and expert weights to e4m3 with a float32 scale for each block of 128

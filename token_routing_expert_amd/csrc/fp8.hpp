@@ -29,8 +29,6 @@ __device__ __forceinline__ void power_scale(uint32_t amax, float& scale, float& 
   inv = __builtin_bit_cast(float, (uint32_t)(127 - (finite ? n : 0)) << 23);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu; }
-
 __device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float d) {
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);

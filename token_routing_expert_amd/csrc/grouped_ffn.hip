@@ -44,7 +44,7 @@
 //     output rows itself (routing weight applied, as the combine would).
 // float32 path (v_mfma_f32_32x32x2_f32): 64 x 128 tiles of four waves,
 // double-buffered k-stages staged through registers into LDS.
-#include "common.hpp"
+#include "keep8.hpp"
 
 #include <algorithm>
 #include <type_traits>
@@ -66,7 +66,16 @@ constexpr int kEpiSwigluSave = 2;  // as kEpiSwiglu, and Out2 = [A Wg | A Wu] (r
 constexpr int kEpiSwigluBwd = 3;   // Out = [dg | du] from dh = A W and Aux = [g | u] (row strides 2N)
 constexpr int kEpiPartial = 4;     // Part[split] = A W over the split's k-stages (float32, row stride N)
 constexpr int kEpiScatter = 5;     // Out[row_token[r]] = row_w[r] * bf16(A W)[r] (one pair per token)
+constexpr int kEpiKeep8 = 6;       // as kEpiSwiglu, and the checkpoint of [A Wg | A Wu] (Kept)
+constexpr int kEpiKeep16 = 7;      // the checkpoint in 16-bit codes, nothing else
+constexpr int kEpiBwd8 = 8;        // Out = w [dg | du] (row stride 2N), Out2 = w h from dh = A W and the checkpoint
+constexpr int kEpiBwd16 = 9;       // as kEpiBwd8 from 16-bit codes
 constexpr int kBwdBlocks = 1;      // column blocks whose g, u the backward epilogue loads together
+
+// epilogues of a gate/up product: tiles of 128 gate and the matching 128 up columns
+constexpr bool is_gate_up(int epi) {
+  return epi == kEpiSwiglu || epi == kEpiSwigluSave || epi == kEpiKeep8 || epi == kEpiKeep16;
+}
 
 __device__ __forceinline__ uint2 pack4(const float* f) {
   return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
@@ -172,6 +181,40 @@ struct Tile {
   int n0;
 };
 
+// The rows of one tile in a row-major array of row_bytes a row, behind a buffer
+// descriptor: a lane's offset is 32 bits, what is the same for a wave goes into
+// a scalar, and rows past the tile's are not stored and read as zeros.
+struct TileRows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  __device__ __forceinline__ TileRows(const void* base, int64_t row0, int rows, int row_bytes)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(uniform_ptr((const char*)base + row0 * row_bytes), (short)0,
+                                               __builtin_amdgcn_readfirstlane(rows * row_bytes), kBufferConfig)) {}
+  __device__ __forceinline__ u32x4 load16(uint32_t lane, int scalar) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, scalar, 0);
+  }
+  __device__ __forceinline__ float load4(uint32_t lane, int scalar) const {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane, scalar, 0));
+  }
+  // (The offsets are added here and not left to the instruction: behind a
+  // 16-byte store without a scalar offset the compiler keeps its data registers
+  // for one more instruction.  With one it does not, and the next instruction's
+  // result was seen in the stored rows on gfx950.)
+  __device__ __forceinline__ void store16(u32x4 v, uint32_t lane, int scalar) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, lane + scalar, 0, 0);
+  }
+  __device__ __forceinline__ void store4(float v, uint32_t lane, int scalar) const {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, lane, scalar, 0);
+  }
+};
+
+// Two 4-column groups 8 columns apart in lanes l and l + 32 (pk[group][dword])
+// as the 8 consecutive columns of lane l's group: see swap_store below.
+__device__ __forceinline__ u32x4 eight_columns(const uint32_t (&pk)[2][2]) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pk[0][0], pk[1][0], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pk[0][1], pk[1][1], false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+
 // The tiles of one workgroup form a single stream of k-stages: stage g of
 // the stream lives in ring buffer g % NS, and while stage g is multiplied,
 // stages g+1 .. g+NS-1 are in flight, whichever tiles they belong to -- so
@@ -181,17 +224,18 @@ struct Tile {
 // tile never waits on a plain global load (which would drain the ring).
 // (launch bounds: workgroup size and waves per SIMD -- OCC workgroups of
 // 2 WM waves per CU need OCC WM / 2 of them, at least one)
+// kept: the checkpoint that kEpiKeep8 and kEpiKeep16 write and kEpiBwd8 and kEpiBwd16 read
 template <int EPI, bool BT, int BK, int OCC, int NJ, int WM, int NS, bool PP, bool TL>
 __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     const bf16_t* __restrict__ A, const int32_t* __restrict__ offsets, int64_t max_rows, int E, int K, int N, int ldw,
     const bf16_t* __restrict__ W, bf16_t* __restrict__ Out, int n_tiles, const int32_t* __restrict__ row_token,
     int64_t a_rows, bf16_t* __restrict__ Out2, const bf16_t* __restrict__ Aux, int n_split_arg,
-    float* __restrict__ Part, int32_t* __restrict__ sched, const float* __restrict__ row_w, int wtiled) {
+    float* __restrict__ Part, int32_t* __restrict__ sched, const float* __restrict__ row_w, int wtiled, Kept kept) {
   // (k-split ranges are only used with the lockstep tiles: the ping-pong
   // instances see one range per tile, a constant)
   const int n_split = PP ? 1 : n_split_arg;
   // gate/up tiles: 128 gate columns and the matching 128 up columns
-  constexpr bool SWIGLU = EPI == kEpiSwiglu || EPI == kEpiSwigluSave;
+  constexpr bool SWIGLU = is_gate_up(EPI);
   static_assert(!(SWIGLU && BT), "the gate/up weight is only read as [K][2N]");
   typedef Geo<BK, NJ, WM> GE;
   constexpr int BM = GE::BM, WAVES = GE::WAVES;
@@ -805,6 +849,212 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
             swap_store(pk, orow, c, r < t.rows && c < N);
           }
       }
+    } else if constexpr (EPI == kEpiKeep8 || EPI == kEpiKeep16) {
+      // A wave's 64 gate and 64 up columns are one block of a checkpoint
+      // each (N is a multiple of 64: all of them exist or none).  A row's 32
+      // columns of one MFMA block sit in lanes l and l + 32, 4 at a time: a
+      // lane's maximum over its 32 values and one exchange give the block's.
+      const int c0 = t.n0 + (WCOL / 2) * wn;
+      if (c0 >= N) return;   // (wave-uniform)
+      constexpr bool K8 = EPI == kEpiKeep8;
+      const int nb = N / kKeepBlock;
+      const TileRows q_rows(kept.q, t.row0, t.rows, (K8 ? 2 : 4) * N), s_rows(kept.s, t.row0, t.rows, 8 * nb);
+      const uint32_t h_lane = lr * 2 * N + 4 * lc, q_lane = K8 ? h_lane : lr * 4 * N + 4 * lc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r0 = 64 * wm + 32 * i;
+        if (r0 >= t.rows) continue;  // (wave-uniform)
+        float s[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int j = 0; j < NJ / 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) m = max(m, abs_bits(acc[hf * (NJ / 2) + j][i][q]));
+          const auto sw = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+          float inv;
+          keep_scale<K8 ? 8 : 16>(max(sw[0], sw[1]), s[hf], inv);
+#pragma unroll
+          for (int j = 0; j < NJ / 2; ++j) {
+            const f32x16& v = acc[hf * (NJ / 2) + j][i];
+            const int c = hf * N + c0 + 32 * j;
+            if constexpr (K8) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4)
+                pk[q4] = keep_codes4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3], inv);
+              q_rows.store16(to_halves(pk), q_lane, r0 * 2 * N + c);
+            } else {
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                uint32_t pk[2][2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                  for (int w = 0; w < 2; ++w) {
+                    const int q = 4 * (2 * p + g) + 2 * w;
+                    pk[g][w] = keep_codes2(v[q], v[q + 1], inv);
+                  }
+                q_rows.store16(eight_columns(pk), q_lane, (r0 * 2 * N + c + 16 * p) * 2);
+              }
+            }
+          }
+        }
+        // the lower lane of a row writes the gate block's scale, the upper one the up block's
+        s_rows.store4(lc ? s[1] : s[0], lr * 8 * nb + lc * nb, r0 * 8 * nb + c0 / kKeepBlock * 4);
+        if constexpr (K8) {
+          const TileRows h_rows(Out, t.row0, t.rows, 2 * N);
+#pragma unroll
+          for (int j = 0; j < NJ / 2; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              uint32_t pk[2][2];
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  const int q = 4 * (2 * p + g) + 2 * w;
+                  pk[g][w] = swiglu2(acc[j][i][q], acc[j + NJ / 2][i][q], acc[j][i][q + 1], acc[j + NJ / 2][i][q + 1]);
+                }
+              h_rows.store16(eight_columns(pk), h_lane, (r0 * N + c0 + 32 * j + 16 * p) * 2);
+            }
+        }
+      }
+    } else if constexpr (EPI == kEpiBwd8 || EPI == kEpiBwd16) {
+      // acc is dh (before the row's weight w): with g, u of the row, s =
+      // sigmoid(g) and h = g s u, Out = w [dh u s (1 + g (1 - s)) | dh g s] and
+      // Out2 = w h.  g and u are fetched in units of four 16-byte vectors a
+      // lane, kAhead units before their use, and each lane's share of the
+      // accumulator's columns handed over by lane swaps.
+      constexpr bool K8 = EPI == kEpiBwd8;
+      constexpr int UJ = K8 ? 2 : 1;                  // column blocks of 32 in a unit
+      constexpr int UPI = NJ / UJ, UNITS = 2 * UPI;   // units of a row block; of the wave
+      constexpr int kAhead = 2;
+      const int c0 = t.n0 + WCOL * wn;                // the wave's first column
+      const int nb = N / kKeepBlock;
+      const TileRows dgu_rows(Out, t.row0, t.rows, 4 * N), h_rows(Out2, t.row0, t.rows, 2 * N),
+          gu_rows(kept.q, t.row0, t.rows, (K8 ? 2 : 4) * N),
+          s_rows(kept.s, t.row0, t.rows, 8 * nb);
+      const uint32_t dgu_lane = lr * 4 * N + 4 * lc, h_lane = lr * 2 * N + 4 * lc,
+                     gu_lane = K8 ? h_lane : dgu_lane;   // (16 columns of 1 byte a lane, or 8 of 2)
+      u32x4 raw[kAhead + 1][2][2];                    // [unit][g or u][column block, or half of one]
+      float sc[kAhead + 1][2];
+      auto fetch = [&](auto u_c) {
+        constexpr int u = decltype(u_c)::value;
+        constexpr int j0 = (u % UPI) * UJ, b = u % (kAhead + 1);
+        const int r0 = 64 * wm + 32 * (u / UPI);
+        // (columns past N: the tile's first ones are read, and nothing is stored)
+        const int c = c0 + 32 * j0 < N ? c0 + 32 * j0 : t.n0;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+            raw[b][hf][v] = gu_rows.load16(gu_lane, K8 ? r0 * 2 * N + hf * N + c + 32 * v
+                                                       : (r0 * 2 * N + hf * N + c + 16 * v) * 2);
+          sc[b][hf] = s_rows.load4(lr * 8 * nb, (r0 * 2 + hf) * nb * 4 + c / kKeepBlock * 4);
+        }
+      };
+      float sum = 0.f, w = 1.f;
+      auto unit = [&](auto u_c) {
+        constexpr int u = decltype(u_c)::value;
+        constexpr int i = u / UPI, j0 = (u % UPI) * UJ, b = u % (kAhead + 1);
+        __builtin_amdgcn_sched_barrier(0);   // (one unit's temporaries at a time: registers)
+        if constexpr (u + kAhead < UNITS) fetch(std::integral_constant<int, u + kAhead>{});
+        const int r0 = 64 * wm + 32 * i;
+        if constexpr (u % UPI == 0) {
+          sum = 0.f;
+          if (row_w) w = TileRows(row_w, t.row0, t.rows, 4).load4(lr * 4, r0 * 4);
+        }
+#pragma unroll
+        for (int jj = 0; jj < UJ; ++jj) {
+          const int j = j0 + jj;
+          const bool there = c0 + 32 * j < N;   // (wave-uniform)
+          uint32_t gq[2][4], uq[2][4];          // 8 bits: [0]; 16: the two dwords of 4 columns
+          if constexpr (K8) {
+            from_halves(raw[b][0][jj], gq[0]);
+            from_halves(raw[b][1][jj], uq[0]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              from_quarters(raw[b][0][v], gq, 2 * v);
+              from_quarters(raw[b][1][v], uq, 2 * v);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint32_t pg[2][2], pu[2][2], ph[2][2];   // [4-column group][dword]
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int q4 = 2 * p + q;
+              float g[4], u4[4], dg[4], du[4], h[4];
+              if constexpr (K8) {
+                keep_values4(gq[0][q4], sc[b][0], g);
+                keep_values4(uq[0][q4], sc[b][1], u4);
+              } else {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  keep_values2(gq[v][q4], sc[b][0], g + 2 * v);
+                  keep_values2(uq[v][q4], sc[b][1], u4 + 2 * v);
+                }
+              }
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const float dh = acc[j][i][4 * q4 + v];
+                const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-g[v]));
+                const float silu = g[v] * sg;
+                h[v] = silu * u4[v];
+                sum = fmaf(h[v], there ? dh : 0.f, sum);
+                const float wdh = w * dh;
+                dg[v] = wdh * u4[v] * (sg + silu * (1.f - sg));
+                du[v] = wdh * silu;
+                h[v] *= w;
+              }
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                pg[q][v] = pack_bf16x2(dg[2 * v], dg[2 * v + 1]);
+                pu[q][v] = pack_bf16x2(du[2 * v], du[2 * v + 1]);
+                ph[q][v] = pack_bf16x2(h[2 * v], h[2 * v + 1]);
+              }
+            }
+            asm volatile("" : "+v"(sum));   // (summed here: left to the store below, every h stays in a register)
+            const u32x4 vg = eight_columns(pg), vu = eight_columns(pu), vh = eight_columns(ph);
+            if (there) {
+              const int c = c0 + 32 * j + 16 * p;
+              dgu_rows.store16(vg, dgu_lane, (r0 * 2 * N + c) * 2);
+              dgu_rows.store16(vu, dgu_lane, (r0 * 2 * N + N + c) * 2);
+              h_rows.store16(vh, h_lane, (r0 * N + c) * 2);
+            }
+          }
+        }
+        if constexpr (u % UPI == UPI - 1) {
+          if (Part) {
+            // <dh, h> over the wave's columns: the row's other 4-column groups are in lane l + 32
+            const uint32_t bits = __builtin_bit_cast(uint32_t, sum);
+            const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+            const uint32_t lo = sw[0], hi = sw[1];
+            const int parts = 2 * n_tiles;
+            TileRows(Part, t.row0, t.rows, 4 * parts)
+                .store4(__builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi),
+                        lc == 0 ? lr * 4 * parts : kOutOfRange, (r0 * parts + 2 * (t.n0 / BNO) + wn) * 4);
+          }
+        }
+      };
+      if (64 * wm < t.rows) {   // (wave-uniform, as below)
+        fetch(std::integral_constant<int, 0>{});
+        if constexpr (kAhead > 1) fetch(std::integral_constant<int, 1>{});
+        auto row_block = [&](auto i_c) {
+          constexpr int u0 = decltype(i_c)::value * UPI;
+          unit(std::integral_constant<int, u0>{});
+          unit(std::integral_constant<int, u0 + 1>{});
+          if constexpr (UPI > 2) {
+            unit(std::integral_constant<int, u0 + 2>{});
+            unit(std::integral_constant<int, u0 + 3>{});
+          }
+        };
+        row_block(std::integral_constant<int, 0>{});
+        if (64 * wm + 32 < t.rows) row_block(std::integral_constant<int, 1>{});
+      }
     } else if constexpr (EPI == kEpiPlain || EPI == kEpiScatter) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -852,7 +1102,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (EPI == kEpiSwiglu || EPI == kEpiPlain || EPI == kEpiScatter) break;
+      if (EPI == kEpiSwiglu || EPI == kEpiPlain || EPI == kEpiScatter || EPI >= kEpiKeep8) break;
       const int r = 64 * wm + 32 * i + lr;
       if (r >= t.rows) continue;
       bf16_t* orow = Out + (t.row0 + r) * N;
@@ -1226,6 +1476,9 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     else
       epilogue(cur, (int)(cur_u % n_split), c_tile % NSLOT);
     zero_acc();
+    // (a wave with nothing to multiply leaves the fragments as they are: set
+    // here, they need not live through an epilogue that is short of registers)
+    if constexpr (EPI >= kEpiKeep8) f0 = f1 = Frag{};
     const int64_t u = unit_of(c_tile + 1);
     if (u < 0) break;
     cur = decode(unit_tile(u), c_cursor);
@@ -1540,15 +1793,15 @@ hipError_t launch_dma(const bf16_t* a, const int32_t* offsets, int64_t max_rows,
                       const bf16_t* w, bf16_t* out, hipStream_t s, const int32_t* row_token = nullptr,
                       int64_t a_rows = 0, bf16_t* out2 = nullptr, const bf16_t* aux = nullptr, int n_split = 1,
                       float* part = nullptr, int32_t* sched = nullptr, const float* row_w = nullptr,
-                      bool wtiled = false) {
-  constexpr bool SWIGLU = EPI == kEpiSwiglu || EPI == kEpiSwigluSave;
+                      bool wtiled = false, Kept kept = {}) {
+  constexpr bool SWIGLU = is_gate_up(EPI);
   constexpr int BNO = SWIGLU ? 32 * NJ : 64 * NJ;   // output columns per tile
   if (K / BK / n_split < NS - 1) return hipErrorInvalidValue;  // each range spans at least NS - 1 stages
   const int nt = (int)ceil_div(N, BNO);
   dma::k_grouped_gemm<EPI, BT, BK, OCC, NJ, WM, NS, PP, TL>
       <<<persistent_grid(max_rows, E, 64 * WM, nt * n_split, OCC), 128 * WM, 0, s>>>(
           a, offsets, max_rows, E, K, N, ldw, w, out, nt, row_token, a_rows, out2, aux, n_split, part, sched, row_w,
-          wtiled ? 1 : 0);
+          wtiled ? 1 : 0, kept);
   return hipGetLastError();
 }
 
@@ -1662,7 +1915,7 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
                        const bf16_t* w, bf16_t* out, hipStream_t s, const int32_t* row_token = nullptr,
                        int64_t a_rows = 0, bf16_t* out2 = nullptr, const bf16_t* aux = nullptr,
                        int32_t* sched = nullptr, float* tail_ws = nullptr, bool allow_tall = true,
-                       bool wtiled = false);
+                       bool wtiled = false, const float* row_w = nullptr, const Kept& kept = {});
 
 // 256-row tiles (8 waves in ping-pong, one workgroup per CU: each weight
 // stage feeds twice the rows) once the experts hold 128 rows or more on
@@ -1688,7 +1941,11 @@ template <int EPI, bool BT>
 hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows, int E, int K, int N, int ldw,
                        const bf16_t* w, bf16_t* out, hipStream_t s, const int32_t* row_token, int64_t a_rows,
                        bf16_t* out2, const bf16_t* aux, int32_t* sched, float* tail_ws, bool allow_tall,
-                       bool wtiled) {
+                       bool wtiled, const float* row_w, const Kept& kept) {
+  // (Part: a tail workspace for the down projection, the dot products of the backward's epilogue)
+  constexpr bool kPart = (EPI == kEpiPlain && !BT) || EPI == kEpiBwd8 || EPI == kEpiBwd16;
+  constexpr bool kRowPart = kPart && EPI != kEpiPlain;   // (split tails are the 256-row tiles')
+  float* part = kPart ? tail_ws : nullptr;
   if constexpr (EPI == kEpiPlain && !BT) {
     if (allow_tall && big_tiles(max_rows, E, K) && tall_tiles(max_rows, E) && row_token == nullptr)
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, nullptr,
@@ -1701,13 +1958,13 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
   }
   if (big_tiles(max_rows, E, K))
     return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
-                                                     a_rows, out2, aux, 1, EPI == kEpiPlain && !BT ? tail_ws : nullptr,
-                                                     sched, nullptr, wtiled);
+                                                     a_rows, out2, aux, 1, part, sched, row_w, wtiled, kept);
   if (small_tiles(max_rows, E))
     return launch_dma<EPI, BT, 32, 2, 4, 1, 3, false>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
-                                                      a_rows, out2, aux, 1, nullptr, nullptr, nullptr, wtiled);
-  return launch_dma<EPI, BT>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token, a_rows, out2, aux, 1, nullptr,
-                             nullptr, nullptr, wtiled);
+                                                      a_rows, out2, aux, 1, kRowPart ? part : nullptr, nullptr, row_w,
+                                                      wtiled, kept);
+  return launch_dma<EPI, BT>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token, a_rows, out2, aux, 1,
+                             kRowPart ? part : nullptr, nullptr, row_w, wtiled, kept);
 }
 
 }  // namespace
@@ -1804,6 +2061,33 @@ hipError_t launch_down_dgrad_swiglu_bf16(const bf16_t* dy, const int32_t* expert
                                           nullptr, gu);
 }
 
+hipError_t launch_gate_up_keep8_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                     int I, const bf16_t* w_gate_up, bf16_t* h, const Kept& kept, hipStream_t s,
+                                     const int32_t* row_token, int64_t x_rows, int32_t* sched) {
+  return launch_auto<kEpiKeep8, false>(x, expert_offsets, max_rows, E, d, I, 2 * I, w_gate_up, h, s, row_token, x_rows,
+                                       nullptr, nullptr, sched, nullptr, true, false, nullptr, kept);
+}
+
+hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                      int I, const bf16_t* w_gate_up, const Kept& kept, hipStream_t s,
+                                      int32_t* sched) {
+  return launch_auto<kEpiKeep16, false>(x, expert_offsets, max_rows, E, d, I, 2 * I, w_gate_up, nullptr, s, nullptr, 0,
+                                        nullptr, nullptr, sched, nullptr, true, false, nullptr, kept);
+}
+
+int64_t dot_parts(int I) { return 2 * ceil_div(I, 256); }
+
+hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
+                                bf16_t* h, float* dot, hipStream_t s, const int32_t* row_token, int64_t dy_rows) {
+  // dh = dy Wd^T: Wd [I][d] is the [N][K] weight of a product with K = d, N = I
+  if (bits == 16)
+    return launch_auto<kEpiBwd16, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, row_token, dy_rows, h,
+                                        nullptr, nullptr, dot, true, false, row_w, kept);
+  return launch_auto<kEpiBwd8, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, row_token, dy_rows, h,
+                                     nullptr, nullptr, dot, true, false, row_w, kept);
+}
+
 hipError_t launch_gate_up_dgrad_bf16(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,
                                      int d, int I, const bf16_t* w_gate_up, bf16_t* dx_perm, hipStream_t s) {
   // dx = [dg | du] Wgu^T: Wgu [d][2I] is the [N][K] weight of a product with K = 2I, N = d
@@ -1891,6 +2175,11 @@ hipError_t launch_down_dgrad_swiglu_f32(const float* dy, const int32_t* expert_o
                                         hipStream_t s) {
   // dh = dy Wd^T: Wd [I][d] is the [N][K] weight of a product with K = d, N = I
   return launch_f32<kF32SwigluBwd, true>(dy, expert_offsets, max_rows, E, d, I, w_down, dgu, s, nullptr, gu);
+}
+
+hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 const float* w_down, float* dh, hipStream_t s) {
+  return launch_f32<kF32Epi, true>(dy, expert_offsets, max_rows, E, d, I, w_down, dh, s);
 }
 
 hipError_t launch_gate_up_dgrad_f32(const float* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,

@@ -1,0 +1,238 @@
+// train.hip -- the steps of the training operators beside the products: the
+// 8-bit checkpoint of float32 rows and its values, the float32 SwiGLU
+// backward, the grouped rows of x and dout, and the routing weights' gradients.
+// (In bf16 the checkpoint is written and read, and the SwiGLU backward done, in
+// the products' epilogues, grouped_ffn.hip.)
+#include "keep8.hpp"
+
+namespace tre {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
+
+// max over 16 consecutive lanes (quads, then mirrored halves)
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));   // mirror in 8 lanes
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror in 16 lanes
+}
+
+// 16 lanes take a block of 64, four values each.
+__global__ __launch_bounds__(kThreads) void k_keep8_f32(const float* __restrict__ gu,
+                                                        const int32_t* __restrict__ offsets, int E, int64_t max_rows,
+                                                        int nb, Kept kept) {
+  const int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 16;   // block of the checkpoint (nb a row)
+  const int64_t rows = clampi<int64_t>(offsets[E], 0, max_rows);
+  if (b >= rows * nb) return;   // (the same for a block's 16 lanes)
+  const int l16 = threadIdx.x % 16;
+  const f32x4 v = *(const f32x4*)(gu + b * kKeepBlock + 4 * l16);
+  const uint32_t m = max16(max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3]))));
+  float s, inv;
+  keep_scale(m, s, inv);
+  *(uint32_t*)(kept.q + b * kKeepBlock + 4 * l16) = keep_codes4(v[0], v[1], v[2], v[3], inv);
+  if (l16 == 0) kept.s[b] = s;
+}
+
+// 16 codes a thread.
+template <typename Elem>
+__global__ __launch_bounds__(kThreads) void k_keep8_values(Kept kept, int64_t n_vec, Elem* __restrict__ gu) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n_vec) return;
+  const u32x4 q = ((const u32x4*)kept.q)[i];
+  const float s = kept.s[i / (kKeepBlock / 16)];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[8];
+    const uint32_t q0 = q[2 * h], q1 = q[2 * h + 1];
+    keep_values4(q0, s, v);
+    keep_values4(q1, s, v + 4);
+    if constexpr (sizeof(Elem) == 4) {
+      *(f32x4*)(gu + 16 * i + 8 * h) = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4*)(gu + 16 * i + 8 * h + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *(u32x4*)(gu + 16 * i + 8 * h) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+  }
+}
+
+// One wave a grouped row, four columns a lane: the SwiGLU backward of
+// include/moe_training.h in float32, and the row's <dh, h>.
+template <bool K8>
+__global__ __launch_bounds__(kThreads) void k_swiglu_bwd_f32(const float* __restrict__ dh, const float* __restrict__ gu,
+                                                             Kept kept, const float* __restrict__ row_w,
+                                                             const int32_t* __restrict__ offsets, int E,
+                                                             int64_t max_rows, int I, float* __restrict__ dgu,
+                                                             float* __restrict__ h, float* __restrict__ dot) {
+  const int64_t r = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+  if (r >= clampi<int64_t>(offsets[E], 0, max_rows)) return;
+  const int lane = threadIdx.x % kWave;
+  const float w = row_w ? row_w[r] : 1.f;
+  float sum = 0.f;
+  for (int c = 4 * lane; c < I; c += 4 * kWave) {
+    float g[4], u[4];
+    if constexpr (K8) {
+      const int nb = I / kKeepBlock;
+      keep_values4(*(const uint32_t*)(kept.q + r * 2 * I + c), kept.s[r * 2 * nb + c / kKeepBlock], g);
+      keep_values4(*(const uint32_t*)(kept.q + r * 2 * I + I + c), kept.s[r * 2 * nb + nb + c / kKeepBlock], u);
+    } else {
+      const f32x4 a = *(const f32x4*)(gu + r * 2 * I + c), b = *(const f32x4*)(gu + r * 2 * I + I + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = a[i], u[i] = b[i];
+    }
+    const f32x4 d = *(const f32x4*)(dh + r * I + c);
+    f32x4 dg, du, hv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float sg = 1.f / (1.f + expf(-g[i]));
+      const float silu = g[i] * sg, wd = w * d[i];
+      sum = fmaf(silu * u[i], d[i], sum);
+      dg[i] = wd * u[i] * (sg + silu * (1.f - sg));
+      du[i] = wd * silu;
+      hv[i] = w * (silu * u[i]);
+    }
+    *(f32x4*)(dgu + r * 2 * I + c) = dg;
+    *(f32x4*)(dgu + r * 2 * I + I + c) = du;
+    *(f32x4*)(h + r * I + c) = hv;
+  }
+  if (!dot) return;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  if (lane == 0) dot[r] = sum;
+}
+
+// One wave a token: its rows of x and dout to every grouped row its pairs have,
+// and those rows' routing weights.
+__global__ __launch_bounds__(kThreads) void k_pair_rows(const u32x4* __restrict__ x, const u32x4* __restrict__ dout,
+                                                        int64_t T, int k, int64_t vec_per_row,
+                                                        const int32_t* __restrict__ pair_row,
+                                                        const float* __restrict__ pair_w, int64_t max_rows,
+                                                        u32x4* __restrict__ x_perm, u32x4* __restrict__ dout_perm,
+                                                        float* __restrict__ row_w) {
+  const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+  if (t >= T) return;
+  const int lane = threadIdx.x % kWave;
+  constexpr int kVec = 4;
+  for (int64_t base = lane; base < vec_per_row; base += kVec * kWave) {
+    u32x4 a[kVec], b[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int64_t v = base + i * kWave;
+      if (v < vec_per_row) {
+        a[i] = x[t * vec_per_row + v];
+        b[i] = dout[t * vec_per_row + v];
+      }
+    }
+    for (int j = 0; j < k; ++j) {
+      const int64_t r = pair_row[t * k + j];
+      MOE_DCHECK(r >= -1 && r < max_rows);
+      if (r < 0 || r >= max_rows) continue;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int64_t v = base + i * kWave;
+        if (v < vec_per_row) {
+          x_perm[r * vec_per_row + v] = a[i];
+          dout_perm[r * vec_per_row + v] = b[i];
+        }
+      }
+    }
+  }
+  for (int j = lane; j < k; j += kWave) {
+    const int64_t r = pair_row[t * k + j];
+    if (r >= 0 && r < max_rows) row_w[r] = pair_w[t * k + j];
+  }
+}
+
+// One wave a token: dw[p] = the sum of row pair_row[p]'s parts (lanes take
+// them in turn, then the wave's sum), and through the softmax of the selected
+// logits dlogits[t, e] = the sum over the pairs p of e of w_p (dw_p - sum_i w_i dw_i).
+__global__ __launch_bounds__(kThreads) void k_pair_grad(const float* __restrict__ dot, int64_t n_parts,
+                                                        int64_t max_rows, const int32_t* __restrict__ pair_row,
+                                                        const float* __restrict__ pair_w,
+                                                        const int32_t* __restrict__ topk_idx, int64_t T, int k, int E,
+                                                        float* __restrict__ dw, float* __restrict__ dlogits) {
+  // with dlogits k <= E; every lane of a wave writes the same value and reads
+  // back only what it wrote itself
+  __shared__ float s_dw[kWaves][kMaxExperts];
+  const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+  if (t >= T) return;
+  const int lane = threadIdx.x % kWave;
+  float* my_dw = s_dw[threadIdx.x / kWave];
+  float inner = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = pair_row[t * k + j];
+    MOE_DCHECK(r >= -1 && r < max_rows);
+    float sum = 0.f;
+    if (r >= 0 && r < max_rows) {
+      for (int64_t n = lane; n < n_parts; n += kWave) sum += dot[r * n_parts + n];
+#pragma unroll
+      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    }
+    if (lane == 0) dw[t * k + j] = sum;
+    if (dlogits) my_dw[j] = sum;
+    inner = fmaf(pair_w[t * k + j], sum, inner);
+  }
+  if (!dlogits) return;
+  for (int e = lane; e < E; e += kWave) {
+    float v = 0.f;
+    for (int j = 0; j < k; ++j)
+      if (topk_idx[t * k + j] == e) v += pair_w[t * k + j] * (my_dw[j] - inner);
+    dlogits[t * E + e] = v;
+  }
+}
+
+unsigned blocks_of(int64_t n, int64_t per) { return (unsigned)ceil_div(n, per); }
+
+}  // namespace
+
+hipError_t launch_keep8_f32(const float* gu, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
+                            const Kept& kept, hipStream_t s) {
+  const int nb = 2 * I / kKeepBlock;
+  k_keep8_f32<<<blocks_of(max_rows * nb, kThreads / 16), kThreads, 0, s>>>(gu, expert_offsets, E, max_rows, nb, kept);
+  return hipGetLastError();
+}
+
+hipError_t launch_keep8_values_f32(const Kept& kept, int64_t rows, int I, float* gu, hipStream_t s) {
+  const int64_t n_vec = rows * 2 * I / 16;
+  k_keep8_values<float><<<blocks_of(n_vec, kThreads), kThreads, 0, s>>>(kept, n_vec, gu);
+  return hipGetLastError();
+}
+
+hipError_t launch_keep8_values_bf16(const Kept& kept, int64_t rows, int I, bf16_t* gu, hipStream_t s) {
+  const int64_t n_vec = rows * 2 * I / 16;
+  k_keep8_values<bf16_t><<<blocks_of(n_vec, kThreads), kThreads, 0, s>>>(kept, n_vec, gu);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& kept, const float* row_w,
+                                 const int32_t* expert_offsets, int E, int64_t max_rows, int I, float* dgu, float* h,
+                                 float* dot, hipStream_t s) {
+  const unsigned blocks = blocks_of(max_rows, kWaves);
+  if (gu)
+    k_swiglu_bwd_f32<false><<<blocks, kThreads, 0, s>>>(dh, gu, kept, row_w, expert_offsets, E, max_rows, I, dgu, h,
+                                                        dot);
+  else
+    k_swiglu_bwd_f32<true><<<blocks, kThreads, 0, s>>>(dh, gu, kept, row_w, expert_offsets, E, max_rows, I, dgu, h,
+                                                       dot);
+  return hipGetLastError();
+}
+
+hipError_t launch_pair_rows(const void* x, const void* dout, int64_t T, int k, int64_t row_bytes,
+                            const int32_t* pair_row, const float* pair_w, int64_t max_rows, void* x_perm,
+                            void* dout_perm, float* row_w, hipStream_t s) {
+  k_pair_rows<<<blocks_of(T, kWaves), kThreads, 0, s>>>((const u32x4*)x, (const u32x4*)dout, T, k, row_bytes / 16,
+                                                        pair_row, pair_w, max_rows, (u32x4*)x_perm,
+                                                        (u32x4*)dout_perm, row_w);
+  return hipGetLastError();
+}
+
+hipError_t launch_pair_grad(const float* dot, int64_t n_parts, int64_t max_rows, const int32_t* pair_row,
+                            const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int E, float* dw,
+                            float* dlogits, hipStream_t s) {
+  k_pair_grad<<<blocks_of(T, kWaves), kThreads, 0, s>>>(dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, E,
+                                                        dw, dlogits);
+  return hipGetLastError();
+}
+
+}  // namespace tre
