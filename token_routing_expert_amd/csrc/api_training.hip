@@ -103,8 +103,9 @@ GradLayout grad_layout(int64_t rows, int64_t I, moe_dtype dt, bool again) {
   return L;
 }
 
-// The layer's backward around them: the grouped rows of x and dout, their
-// weights, the dot products' parts, and the rows' dx.
+// The layer's backward around them: the rows' weights, the dot products' parts
+// and the rows' dx (float32: a token's sum is rounded once), and the grouped rows
+// of x and dout.
 struct BackwardLayout {
   size_t x_perm, dout_perm, row_w, dot, dx_perm, grad, total;
 };
@@ -113,14 +114,14 @@ int64_t dot_columns(int64_t I, moe_dtype dt) { return dt == MOE_F32 ? 1 : dot_pa
 
 BackwardLayout backward_layout(int64_t T, int64_t d, int64_t k, int64_t I, moe_dtype dt) {
   const int64_t P = T * k;
-  const size_t s = elem_size(dt);
+  const size_t copy = align256((size_t)(P * d) * elem_size(dt));
   BackwardLayout L;
   size_t o = 0;
-  L.x_perm = o;    o += align256((size_t)(P * d) * s);
-  L.dout_perm = o; o += align256((size_t)(P * d) * s);
+  L.x_perm = o;    o += copy;
+  L.dout_perm = o; o += copy;
   L.row_w = o;     o += align256((size_t)P * 4);
   L.dot = o;       o += align256((size_t)(P * dot_columns(I, dt)) * 4);
-  L.dx_perm = o;   o += align256((size_t)(P * d) * s);
+  L.dx_perm = o;   o += align256((size_t)(P * d) * 4);
   L.grad = o;      o += grad_layout(P, I, dt, false).total;
   L.total = o;
   return L;
@@ -134,34 +135,20 @@ moe_status zero_weight_gradients(int32_t E, int32_t d, int32_t I, moe_dtype dt, 
   return from_hip(launch_zero_bf16((bf16_t*)dw_down, (int64_t)E * I * d * halves, s));
 }
 
-// The gradients of grouped rows x with dy (times row_w): from the checkpoint,
-// or, where kept.q is null, from g | u computed again.  dot: see launch_down_bwd_bf16.
-moe_status grad_rows(const void* x, const void* dy, const float* row_w, const int32_t* offs, int64_t rows, int32_t E,
-                     int32_t d, int32_t I, const void* w_gate_up, const void* w_down, moe_dtype dt, const Kept& kept,
-                     void* dx, void* dw_gate_up, void* dw_down, float* dot, char* ws, const GradLayout& L,
-                     hipStream_t s) {
+// The gradients of grouped rows x with dy (times row_w), float32: from the
+// checkpoint, or, where kept.q is null, from g | u computed again.
+moe_status grad_rows_f32(const float* x, const float* dy, const float* row_w, const int32_t* offs, int64_t rows,
+                         int32_t E, int32_t d, int32_t I, const float* wgu, const float* wd, const Kept& kept,
+                         float* dx, float* dw_gate_up, float* dw_down, float* dot, char* ws, const GradLayout& L,
+                         hipStream_t s) {
   const bool again = kept.q == nullptr;
-  if (dt == MOE_F32) {
-    const float *fx = (const float*)x, *fdy = (const float*)dy, *fwgu = (const float*)w_gate_up,
-                *fwd = (const float*)w_down;
-    float *h = (float*)(ws + L.h), *dgu = (float*)(ws + L.dgu), *gu = (float*)(ws + L.gu), *dh = (float*)(ws + L.dh);
-    if (again) TRY(from_hip(launch_gate_up_save_f32(fx, offs, rows, E, d, I, fwgu, h, gu, s)));
-    TRY(from_hip(launch_down_dgrad_f32(fdy, offs, rows, E, d, I, fwd, dh, s)));
-    TRY(from_hip(launch_swiglu_bwd_f32(dh, again ? gu : nullptr, kept, row_w, offs, E, rows, I, dgu, h, dot, s)));
-    TRY(from_hip(launch_wgrad_f32(h, I, I, fdy, d, d, offs, rows, E, (float*)dw_down, s)));
-    TRY(from_hip(launch_gate_up_dgrad_f32(dgu, offs, rows, E, d, I, fwgu, (float*)dx, s)));
-    return from_hip(launch_wgrad_f32(fx, d, d, dgu, 2 * I, 2 * I, offs, rows, E, (float*)dw_gate_up, s));
-  }
-  const bf16_t *bx = (const bf16_t*)x, *bdy = (const bf16_t*)dy, *wgu = (const bf16_t*)w_gate_up,
-               *wd = (const bf16_t*)w_down;
-  bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
-  const Kept own{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s)};
-  if (again) TRY(from_hip(launch_gate_up_keep16_bf16(bx, offs, rows, E, d, I, wgu, own, s, nullptr)));
-  TRY(from_hip(launch_down_bwd_bf16(bdy, offs, rows, E, d, I, wd, again ? own : kept, again ? 16 : 8, row_w, dgu, h,
-                                    dot, s, nullptr, 0)));
-  TRY(from_hip(launch_wgrad_bf16(h, I, I, bdy, d, d, offs, rows, E, (bf16_t*)dw_down, s)));
-  TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, offs, rows, E, d, I, wgu, (bf16_t*)dx, s)));
-  return from_hip(launch_wgrad_bf16(bx, d, d, dgu, 2 * I, 2 * I, offs, rows, E, (bf16_t*)dw_gate_up, s));
+  float *h = (float*)(ws + L.h), *dgu = (float*)(ws + L.dgu), *gu = (float*)(ws + L.gu), *dh = (float*)(ws + L.dh);
+  if (again) TRY(from_hip(launch_gate_up_save_f32(x, offs, rows, E, d, I, wgu, h, gu, s)));
+  TRY(from_hip(launch_down_dgrad_f32(dy, offs, rows, E, d, I, wd, dh, s)));
+  TRY(from_hip(launch_swiglu_bwd_f32(dh, again ? gu : nullptr, kept, row_w, offs, E, rows, I, dgu, h, dot, s)));
+  TRY(from_hip(launch_wgrad_f32(h, I, I, dy, d, d, offs, rows, E, dw_down, s)));
+  TRY(from_hip(launch_gate_up_dgrad_f32(dgu, offs, rows, E, d, I, wgu, dx, s)));
+  return from_hip(launch_wgrad_f32(x, d, d, dgu, 2 * I, 2 * I, offs, rows, E, dw_gate_up, s));
 }
 
 }  // namespace
@@ -221,9 +208,23 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
   if (!aligned16(x_perm, w_gate_up, w_down, dy_perm, dx_perm, dw_gate_up, dw_down, gu_q, workspace)) return MOE_ERR_ARG;
   const GradLayout L = grad_layout(max_rows, I, dt, true);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  char* ws = (char*)workspace;
   const Kept kept{(int8_t*)gu_q, (float*)gu_s};
-  return grad_rows(x_perm, dy_perm, nullptr, expert_offsets, max_rows, E, d, I, w_gate_up, w_down, dt, kept, dx_perm,
-                   dw_gate_up, dw_down, nullptr, (char*)workspace, L, s);
+  if (dt == MOE_F32)
+    return grad_rows_f32((const float*)x_perm, (const float*)dy_perm, nullptr, expert_offsets, max_rows, E, d, I,
+                         (const float*)w_gate_up, (const float*)w_down, kept, (float*)dx_perm, (float*)dw_gate_up,
+                         (float*)dw_down, nullptr, ws, L, s);
+  const bf16_t *x = (const bf16_t*)x_perm, *dy = (const bf16_t*)dy_perm, *wgu = (const bf16_t*)w_gate_up,
+               *wd = (const bf16_t*)w_down;
+  bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
+  const Kept again{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s)};
+  if (!gu_q)
+    TRY(from_hip(launch_gate_up_keep16_bf16(x, expert_offsets, max_rows, E, d, I, wgu, again, s, nullptr)));
+  TRY(from_hip(launch_down_bwd_bf16(dy, expert_offsets, max_rows, E, d, I, wd, gu_q ? kept : again, gu_q ? 8 : 16,
+                                    nullptr, dgu, h, nullptr, s)));
+  TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, expert_offsets, max_rows, E, d, I, wgu, (bf16_t*)dx_perm, s)));
+  return from_hip(launch_ffn_wgrad_bf16(x, dy, h, dgu, expert_offsets, max_rows, E, d, I,
+                                        (bf16_t*)dw_gate_up, (bf16_t*)dw_down, s));
 }
 
 size_t moe_forward_train_q8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt) {
@@ -307,16 +308,29 @@ moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32
   char* ws = (char*)workspace;
   float *row_w = (float*)(ws + L.row_w), *dot = (float*)(ws + L.dot);
   const Kept kept{(int8_t*)gu_q, (float*)gu_s};
-  TRY(from_hip(launch_pair_rows(x, dout, T, k, (int64_t)d * elem_size(dt), pair_row, topk_w, P, ws + L.x_perm,
-                                ws + L.dout_perm, row_w, s)));
   // the combine's backward puts w_p before dout; it is applied to h and [dg | du] instead, so that dout stays exact
   const GradLayout G = grad_layout(P, I, dt, false);
-  TRY(grad_rows(ws + L.x_perm, ws + L.dout_perm, row_w, expert_offsets, P, E, d, I, w_gate_up, w_down, dt, kept,
-                ws + L.dx_perm, dw_gate_up, dw_down, dot, ws + L.grad, G, s));
-  TRY(from_hip(launch_pair_grad(dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, E, dtopk_w, dlogits, s)));
-  if (dt == MOE_F32)
-    return from_hip(launch_combine_f32((const float*)(ws + L.dx_perm), P, pair_row, nullptr, T, k, d, (float*)dx, s));
-  return from_hip(launch_combine_bf16((const bf16_t*)(ws + L.dx_perm), P, pair_row, nullptr, T, k, d, (bf16_t*)dx, s));
+  char* gws = ws + L.grad;
+  float* dxp = (float*)(ws + L.dx_perm);
+  void *x_perm = ws + L.x_perm, *dout_perm = ws + L.dout_perm;
+  TRY(from_hip(launch_pair_rows(x, dout, T, k, (int64_t)d * elem_size(dt), pair_row, topk_w, P, x_perm, dout_perm,
+                                row_w, s)));
+  if (dt == MOE_F32) {
+    TRY(grad_rows_f32((const float*)x_perm, (const float*)dout_perm, row_w, expert_offsets, P, E, d, I,
+                      (const float*)w_gate_up, (const float*)w_down, kept, dxp, (float*)dw_gate_up, (float*)dw_down,
+                      dot, gws, G, s));
+    return from_hip(launch_combine_grad_f32(dxp, dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
+                                            (float*)dx, dtopk_w, dlogits, s));
+  }
+  const bf16_t *xp = (const bf16_t*)x_perm, *dyp = (const bf16_t*)dout_perm, *wgu = (const bf16_t*)w_gate_up,
+               *wd = (const bf16_t*)w_down;
+  bf16_t *h = (bf16_t*)(gws + G.h), *dgu = (bf16_t*)(gws + G.dgu);
+  TRY(from_hip(launch_down_bwd_bf16(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, s)));
+  TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, s)));
+  TRY(from_hip(launch_ffn_wgrad_bf16(xp, dyp, h, dgu, expert_offsets, P, E, d, I, (bf16_t*)dw_gate_up,
+                                     (bf16_t*)dw_down, s)));
+  return from_hip(launch_combine_grad_bf16(dxp, dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
+                                           (bf16_t*)dx, dtopk_w, dlogits, s));
 }
 
 moe_status moe_checkpoint_values(const void* gu_q, const float* gu_s, int32_t rows, int32_t I, moe_dtype dt, void* gu,

@@ -57,15 +57,27 @@ struct Vec<float> {
   }
 };
 
+// n consecutive elements rounded to Out.
+template <int n>
+__device__ __forceinline__ void store_vec(float* out, const float* f) {
+  *(u32x4*)out = Vec<float>::store(f);
+}
+template <int n>
+__device__ __forceinline__ void store_vec(bf16_t* out, const float* f) {
+  if constexpr (n == 8) *(u32x4*)out = Vec<bf16_t>::store(f);
+  else *(uint2*)out = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+}
+
 // Up to KS slots: each lane first loads its vector of every slot's row (a
 // row index clamped into range, a dropped slot's value discarded by a
 // select), for two vectors at a time, so 2 KS gathers are in flight together.
 // Every expert row is read once: non-temporal loads (measured: the cold
 // combine of the 128-expert layer 47.5 -> 45.3 us).
-template <typename Elem, int KS>
+// (Elem: the rows' type; Out: the output's, which may be narrower.)
+template <typename Elem, int KS, typename Out = Elem>
 __device__ __forceinline__ void combine_token(const u32x4* __restrict__ y, int64_t max_rows,
                                               const int32_t* __restrict__ pair_row, const float* __restrict__ pair_w,
-                                              int64_t t, int k, int64_t vec_per_row, u32x4* __restrict__ out) {
+                                              int64_t t, int k, int64_t vec_per_row, Out* __restrict__ out) {
   constexpr int n = Vec<Elem>::n;
   const int lane = threadIdx.x % kWave;
   int64_t row[KS];
@@ -103,7 +115,7 @@ __device__ __forceinline__ void combine_token(const u32x4* __restrict__ y, int64
 #pragma unroll
         for (int i = 0; i < n; ++i) acc[i] = fmaf(wt[j], f[i], acc[i]);
       }
-      out[t * vec_per_row + v] = Vec<Elem>::store(acc);
+      store_vec<n>(out + (t * vec_per_row + v) * n, acc);
     }
   }
 }
@@ -118,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void k_combine(const u32x4* __restrict__ 
   const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
   if (t >= n_tok) return;
   if constexpr (KS > 0) {
-    combine_token<Elem, KS>(y, max_rows, pair_row, pair_w, t, k, vec_per_row, out);
+    combine_token<Elem, KS>(y, max_rows, pair_row, pair_w, t, k, vec_per_row, (Elem*)out);
     return;
   }
   const int lane = threadIdx.x % kWave;
@@ -189,6 +201,64 @@ __global__ __launch_bounds__(kThreads) void k_combine_bwd(
     float v = 0.f;
     for (int j = 0; j < k; ++j)
       if (topk_idx[t * k + j] == e) v = pair_w[t * k + j] * (my_dw[j] - inner);
+    dlogits[t * E + e] = v;
+  }
+}
+
+// The end of a backward from a checkpoint, one wave per token: dx[t] = the sum
+// of the token's float32 row gradients (rounded to Elem once), dw[p] = the sum
+// of row pair_row[p]'s n_parts dot products (lanes take them in turn, then the
+// wave's sum), and through the softmax of the selected logits dlogits[t, e] =
+// the sum over the pairs p of e of w_p (dw_p - sum_i w_i dw_i).
+// KS > 0: at most KS slots; KS == 0: any k, one slot at a time
+template <typename Elem, int KS>
+__global__ __launch_bounds__(kThreads) void k_combine_grad(
+    const u32x4* __restrict__ dx_perm, const float* __restrict__ dot, int64_t n_parts, int64_t max_rows,
+    const int32_t* __restrict__ pair_row, const float* __restrict__ pair_w, const int32_t* __restrict__ topk_idx,
+    int64_t n_tok, int k, int E, int64_t vec_per_row, Elem* __restrict__ dx, float* __restrict__ dw,
+    float* __restrict__ dlogits) {
+  // with dlogits k <= E; every lane of a wave writes the same value and reads
+  // back only what it wrote itself
+  __shared__ float s_dw[kThreads / kWave][kMaxExperts];
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
+  if (t >= n_tok) return;
+  const int lane = threadIdx.x % kWave;
+  if constexpr (KS > 0) {
+    combine_token<float, KS, Elem>(dx_perm, max_rows, pair_row, nullptr, t, k, vec_per_row, dx);
+  } else {
+    for (int64_t v = lane; v < vec_per_row; v += kWave) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < k; ++j) {
+        const int64_t r = pair_row[t * k + j];
+        if (r < 0 || r >= max_rows) continue;
+        float f[4];
+        Vec<float>::load(dx_perm[r * vec_per_row + v], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += f[i];
+      }
+      store_vec<4>(dx + (t * vec_per_row + v) * 4, acc);
+    }
+  }
+  float* my_dw = s_dw[threadIdx.x / kWave];
+  float inner = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int64_t r = pair_row[t * k + j];
+    MOE_DCHECK(r >= -1 && r < max_rows);
+    float sum = 0.f;
+    if (r >= 0 && r < max_rows) {
+      for (int64_t n = lane; n < n_parts; n += kWave) sum += dot[r * n_parts + n];
+#pragma unroll
+      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+    }
+    if (lane == 0) dw[t * k + j] = sum;
+    if (dlogits) my_dw[j] = sum;
+    inner = fmaf(pair_w[t * k + j], sum, inner);
+  }
+  if (!dlogits) return;
+  for (int e = lane; e < E; e += kWave) {
+    float v = 0.f;
+    for (int j = 0; j < k; ++j)
+      if (topk_idx[t * k + j] == e) v += pair_w[t * k + j] * (my_dw[j] - inner);
     dlogits[t * E + e] = v;
   }
 }
@@ -266,6 +336,35 @@ hipError_t launch_combine_bwd_f32(const float* dout, const float* y_perm, int64_
                                   const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                   int k, int d, int E, float* dy_perm, float* dw, float* dlogits, hipStream_t s) {
   return launch_bwd<float>(dout, y_perm, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dy_perm, dw, dlogits, s);
+}
+
+namespace {
+
+template <typename Elem>
+hipError_t launch_grad(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+                       const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int d,
+                       int E, Elem* dx, float* dw, float* dlogits, hipStream_t s) {
+  const unsigned blocks = (unsigned)ceil_div(T, kThreads / kWave);
+  const auto kernel = k <= 4 ? k_combine_grad<Elem, 4> : k <= 8 ? k_combine_grad<Elem, 8> : k_combine_grad<Elem, 0>;
+  kernel<<<blocks, kThreads, 0, s>>>((const u32x4*)dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k,
+                                     E, d / 4, dx, dw, dlogits);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_combine_grad_bf16(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+                                    const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
+                                    int k, int d, int E, bf16_t* dx, float* dw, float* dlogits, hipStream_t s) {
+  return launch_grad<bf16_t>(dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
+                             s);
+}
+
+hipError_t launch_combine_grad_f32(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+                                   const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
+                                   int k, int d, int E, float* dx, float* dw, float* dlogits, hipStream_t s) {
+  return launch_grad<float>(dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
+                            s);
 }
 
 hipError_t launch_zero_unrouted_bf16(const int32_t* pair_row, int64_t max_rows, int64_t T, int d, bf16_t* out,

@@ -328,13 +328,18 @@ hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_off
                                       int I, const bf16_t* w_gate_up, const Kept& kept, hipStream_t s,
                                       int32_t* sched);
 // dgu = w [dg | du] and h = w silu(g) u from dh = dy Wd^T and a checkpoint of 8 or
-// 16 bits; w = row_w[r], 1 where row_w is null.  With row_token, row r's dy is row
-// row_token[r] of dy [dy_rows, d].  dot (optional, [max_rows, dot_parts(I)]): the
-// parts of <dh, silu(g) u> of each row, one for 128 columns, those past I zero
+// 16 bits; w = row_w[r], 1 where row_w is null.  dot (optional, [max_rows,
+// dot_parts(I)]): the parts of <dh, silu(g) u> of each row, one for 128 columns,
+// those past I zero
 int64_t dot_parts(int I);
 hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                                 const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
-                                bf16_t* h, float* dot, hipStream_t s, const int32_t* row_token, int64_t dy_rows);
+                                bf16_t* h, float* dot, hipStream_t s);
+// dw_down[e] = sum of h^T dy and dw_gate_up[e] = sum of x^T dgu over the rows of
+// expert e, in one launch
+hipError_t launch_ffn_wgrad_bf16(const bf16_t* x, const bf16_t* dy, const bf16_t* h, const bf16_t* dgu,
+                                 const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 bf16_t* dw_gate_up, bf16_t* dw_down, hipStream_t s);
 // the checkpoint of gu [rows, 2I] float32 (rows below offsets[E]), and its values
 hipError_t launch_keep8_f32(const float* gu, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
                             const Kept& kept, hipStream_t s);
@@ -345,6 +350,9 @@ hipError_t launch_keep8_values_bf16(const Kept& kept, int64_t rows, int I, bf16_
 hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& kept, const float* row_w,
                                  const int32_t* expert_offsets, int E, int64_t max_rows, int I, float* dgu, float* h,
                                  float* dot, hipStream_t s);
+// launch_gate_up_dgrad_bf16 with float32 rows
+hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,
+                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, hipStream_t s);
 // dh [max_rows, I] = dy Wd^T
 hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                                  const float* w_down, float* dh, hipStream_t s);
@@ -352,11 +360,15 @@ hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets,
 hipError_t launch_pair_rows(const void* x, const void* dout, int64_t T, int k, int64_t row_bytes,
                             const int32_t* pair_row, const float* pair_w, int64_t max_rows, void* x_perm,
                             void* dout_perm, float* row_w, hipStream_t s);
-// dw[p] = the sum of its row's n_parts dot products (0 for a pair without a row); dlogits (optional) as
-// launch_combine_bwd_bf16's
-hipError_t launch_pair_grad(const float* dot, int64_t n_parts, int64_t max_rows, const int32_t* pair_row,
-                            const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int E, float* dw,
-                            float* dlogits, hipStream_t s);
+// dx[t] = the sum of the token's rows of dx_perm [max_rows, d] (float32); dw[p] =
+// the sum of its row's n_parts dot products (0 for a pair without a row); dlogits
+// (optional) as launch_combine_bwd_bf16's
+hipError_t launch_combine_grad_bf16(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+                                    const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
+                                    int k, int d, int E, bf16_t* dx, float* dw, float* dlogits, hipStream_t s);
+hipError_t launch_combine_grad_f32(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+                                   const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
+                                   int k, int d, int E, float* dx, float* dw, float* dlogits, hipStream_t s);
 
 // ---- 8-bit codes and scales (quantize.hip) ----
 // rows and expert weights to e4m3 with a float32 scale for each block of 128

@@ -70,6 +70,7 @@ constexpr int kEpiKeep8 = 6;       // as kEpiSwiglu, and the checkpoint of [A Wg
 constexpr int kEpiKeep16 = 7;      // the checkpoint in 16-bit codes, nothing else
 constexpr int kEpiBwd8 = 8;        // Out = w [dg | du] (row stride 2N), Out2 = w h from dh = A W and the checkpoint
 constexpr int kEpiBwd16 = 9;       // as kEpiBwd8 from 16-bit codes
+constexpr int kEpiRows32 = 10;     // Part = A W (float32, row stride N)
 constexpr int kBwdBlocks = 1;      // column blocks whose g, u the backward epilogue loads together
 
 // epilogues of a gate/up product: tiles of 128 gate and the matching 128 up columns
@@ -1055,6 +1056,23 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
         row_block(std::integral_constant<int, 0>{});
         if (64 * wm + 32 < t.rows) row_block(std::integral_constant<int, 1>{});
       }
+    } else if constexpr (EPI == kEpiRows32) {
+      const TileRows rows(Part, t.row0, t.rows, 4 * N);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r0 = 64 * wm + 32 * i;
+        if (r0 >= t.rows) continue;  // (wave-uniform)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int c = t.n0 + WCOL * wn + 32 * j;
+          if (c >= N) continue;   // (wave-uniform: N is a multiple of 64)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const f32x4 v = {acc[j][i][4 * q4], acc[j][i][4 * q4 + 1], acc[j][i][4 * q4 + 2], acc[j][i][4 * q4 + 3]};
+            rows.store16(__builtin_bit_cast(u32x4, v), lr * 4 * N + 4 * lc, (r0 * N + c + 8 * q4) * 4);
+          }
+        }
+      }
     } else if constexpr (EPI == kEpiPlain || EPI == kEpiScatter) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -1942,8 +1960,8 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
                        const bf16_t* w, bf16_t* out, hipStream_t s, const int32_t* row_token, int64_t a_rows,
                        bf16_t* out2, const bf16_t* aux, int32_t* sched, float* tail_ws, bool allow_tall,
                        bool wtiled, const float* row_w, const Kept& kept) {
-  // (Part: a tail workspace for the down projection, the dot products of the backward's epilogue)
-  constexpr bool kPart = (EPI == kEpiPlain && !BT) || EPI == kEpiBwd8 || EPI == kEpiBwd16;
+  // (Part: a tail workspace for the down projection, the dot products of the backward's epilogue, float32 rows)
+  constexpr bool kPart = (EPI == kEpiPlain && !BT) || EPI >= kEpiBwd8;
   constexpr bool kRowPart = kPart && EPI != kEpiPlain;   // (split tails are the 256-row tiles')
   float* part = kPart ? tail_ws : nullptr;
   if constexpr (EPI == kEpiPlain && !BT) {
@@ -2079,13 +2097,20 @@ int64_t dot_parts(int I) { return 2 * ceil_div(I, 256); }
 
 hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                                 const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
-                                bf16_t* h, float* dot, hipStream_t s, const int32_t* row_token, int64_t dy_rows) {
+                                bf16_t* h, float* dot, hipStream_t s) {
   // dh = dy Wd^T: Wd [I][d] is the [N][K] weight of a product with K = d, N = I
   if (bits == 16)
-    return launch_auto<kEpiBwd16, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, row_token, dy_rows, h,
+    return launch_auto<kEpiBwd16, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, nullptr, 0, h,
                                         nullptr, nullptr, dot, true, false, row_w, kept);
-  return launch_auto<kEpiBwd8, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, row_token, dy_rows, h,
+  return launch_auto<kEpiBwd8, true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dgu, s, nullptr, 0, h,
                                      nullptr, nullptr, dot, true, false, row_w, kept);
+}
+
+hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,
+                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, hipStream_t s) {
+  // as launch_gate_up_dgrad_bf16
+  return launch_auto<kEpiRows32, true>(dgu, expert_offsets, max_rows, E, 2 * I, d, 2 * I, w_gate_up, nullptr, s,
+                                       nullptr, 0, nullptr, nullptr, nullptr, dx_perm);
 }
 
 hipError_t launch_gate_up_dgrad_bf16(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,

@@ -144,44 +144,6 @@ __global__ __launch_bounds__(kThreads) void k_pair_rows(const u32x4* __restrict_
   }
 }
 
-// One wave a token: dw[p] = the sum of row pair_row[p]'s parts (lanes take
-// them in turn, then the wave's sum), and through the softmax of the selected
-// logits dlogits[t, e] = the sum over the pairs p of e of w_p (dw_p - sum_i w_i dw_i).
-__global__ __launch_bounds__(kThreads) void k_pair_grad(const float* __restrict__ dot, int64_t n_parts,
-                                                        int64_t max_rows, const int32_t* __restrict__ pair_row,
-                                                        const float* __restrict__ pair_w,
-                                                        const int32_t* __restrict__ topk_idx, int64_t T, int k, int E,
-                                                        float* __restrict__ dw, float* __restrict__ dlogits) {
-  // with dlogits k <= E; every lane of a wave writes the same value and reads
-  // back only what it wrote itself
-  __shared__ float s_dw[kWaves][kMaxExperts];
-  const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-  if (t >= T) return;
-  const int lane = threadIdx.x % kWave;
-  float* my_dw = s_dw[threadIdx.x / kWave];
-  float inner = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int64_t r = pair_row[t * k + j];
-    MOE_DCHECK(r >= -1 && r < max_rows);
-    float sum = 0.f;
-    if (r >= 0 && r < max_rows) {
-      for (int64_t n = lane; n < n_parts; n += kWave) sum += dot[r * n_parts + n];
-#pragma unroll
-      for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
-    }
-    if (lane == 0) dw[t * k + j] = sum;
-    if (dlogits) my_dw[j] = sum;
-    inner = fmaf(pair_w[t * k + j], sum, inner);
-  }
-  if (!dlogits) return;
-  for (int e = lane; e < E; e += kWave) {
-    float v = 0.f;
-    for (int j = 0; j < k; ++j)
-      if (topk_idx[t * k + j] == e) v += pair_w[t * k + j] * (my_dw[j] - inner);
-    dlogits[t * E + e] = v;
-  }
-}
-
 unsigned blocks_of(int64_t n, int64_t per) { return (unsigned)ceil_div(n, per); }
 
 }  // namespace
@@ -224,14 +186,6 @@ hipError_t launch_pair_rows(const void* x, const void* dout, int64_t T, int k, i
   k_pair_rows<<<blocks_of(T, kWaves), kThreads, 0, s>>>((const u32x4*)x, (const u32x4*)dout, T, k, row_bytes / 16,
                                                         pair_row, pair_w, max_rows, (u32x4*)x_perm,
                                                         (u32x4*)dout_perm, row_w);
-  return hipGetLastError();
-}
-
-hipError_t launch_pair_grad(const float* dot, int64_t n_parts, int64_t max_rows, const int32_t* pair_row,
-                            const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int E, float* dw,
-                            float* dlogits, hipStream_t s) {
-  k_pair_grad<<<blocks_of(T, kWaves), kThreads, 0, s>>>(dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, E,
-                                                        dw, dlogits);
   return hipGetLastError();
 }
 
