@@ -329,7 +329,7 @@ hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_off
                                       int32_t* sched);
 // dgu = w [dg | du] and h = w silu(g) u from dh = dy Wd^T and a checkpoint of 8 or
 // 16 bits; w = row_w[r], 1 where row_w is null.  dot (optional, [max_rows,
-// dot_parts(I)]): the parts of <dh, silu(g) u> of each row, one for 128 columns,
+// dot_parts(I)]): the parts of <dh, silu(g) u> of each row, one for 32 columns,
 // those past I zero
 int64_t dot_parts(int I);
 hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,

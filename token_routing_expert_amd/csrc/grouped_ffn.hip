@@ -71,6 +71,7 @@ constexpr int kEpiKeep16 = 7;      // the checkpoint in 16-bit codes, nothing el
 constexpr int kEpiBwd8 = 8;        // Out = w [dg | du] (row stride 2N), Out2 = w h from dh = A W and the checkpoint
 constexpr int kEpiBwd16 = 9;       // as kEpiBwd8 from 16-bit codes
 constexpr int kEpiRows32 = 10;     // Part = A W (float32, row stride N)
+constexpr int kDotParts = 8;       // dot products of a row that a column tile of kEpiBwd8 writes, one for 32 columns
 constexpr int kBwdBlocks = 1;      // column blocks whose g, u the backward epilogue loads together
 
 // epilogues of a gate/up product: tiles of 128 gate and the matching 128 up columns
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   constexpr bool SCATTER = EPI == kEpiScatter;
   static_assert(!SCATTER || WAVES >= 2, "the row weights are fetched by wave 1");
   constexpr int NSLOT = SCATTER ? 4 : 2;
-  // Tall tiles (TL: the ping-pong plain and gate/up products): an expert's
+  // Tall tiles (TL: the ping-pong products but those that save pre-activations): an expert's
   // last tile also takes up to XR = 32 rows past BM, so that they do not make
   // a tile of their own -- one that would stream the expert's whole weight
   // slice again, and run its whole stage loop, for a few rows.  Waves 0 and 1
@@ -268,8 +269,8 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   // SwiGLU pairs stay in one lane.  The block costs one MFMA per wave and
   // k-step.
   constexpr bool TALL = TL;
-  static_assert(!TL || (PP && (EPI == kEpiPlain || EPI == kEpiSwiglu) && !BT),
-                "tall tiles: ping-pong plain or gate/up products only");
+  static_assert(!TL || (PP && (EPI == kEpiPlain || EPI == kEpiSwiglu || EPI >= kEpiBwd8)),
+                "tall tiles: ping-pong products with an epilogue for the extra rows");
   constexpr int XR = TALL ? 32 : 0;
   constexpr int A_STAGE = GE::A_BYTES + XR * BK * 2;  // LDS bytes of an activation stage
   typedef Geo<2 * BK, NJ, WM> GD;  // the activation geometry of a double-stage
@@ -397,7 +398,8 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   // by exactly one workgroup, so results do not depend on who takes which.
   // (With fewer rounds the tail is a large share of the tiles, and what its
   // balance gains is lost to weight slices no longer shared in one XCD's L2.)
-  const bool dyn = PP && sched != nullptr && n_split == 1 && total_units >= 4 * (int64_t)G && nk >= 2 * NS;
+  // (The products with rows of k for weights are launched without a counter.)
+  const bool dyn = PP && !BT && sched != nullptr && n_split == 1 && total_units >= 4 * (int64_t)G && nk >= 2 * NS;
   const int rs = dyn ? (int)(total_units / G) - 1 : 0;
   const int64_t tail0 = (int64_t)rs * G;
   const int64_t n_tail = total_units - tail0;
@@ -656,7 +658,8 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     // share a slice through L2, the same policy was 5% slower).
 #pragma unroll
     for (int p = 0; p < GE::B_INSTR; ++p) {
-      if constexpr (TALL) dma16s_nt(b_rsrc, b_lds0 + SLOT * GE::B_BYTES + p * WAVES * 1024, b_voff[p], kb);
+      // (rows of k are half a line a stage: the other half is wanted next)
+      if constexpr (TALL && !BT) dma16s_nt(b_rsrc, b_lds0 + SLOT * GE::B_BYTES + p * WAVES * 1024, b_voff[p], kb);
       else dma16s(b_rsrc, b_lds0 + SLOT * GE::B_BYTES + p * WAVES * 1024, b_voff[p], kb);
     }
     ka += kAStep;
@@ -727,6 +730,10 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     const int col = (WCOL / 2) * wn + 16 * wm + (g16 % 2) * (BNB / 2) + 4 * (L % 4);
     fbx = lds_address(sB) + GE::b_byte(kr, col >> 3) + ((col >> 2) & 1) * 8;
     asm("" : "+v"(fbx));
+  } else if constexpr (TALL && BT) {
+    // the wave's wm-th column block, at k-step 0 (k-step 1's chunk c + 2 of the row sits at the address XOR 32)
+    fbx = lds_address(sB) + GE::a_byte(WCOL * wn + 32 * wm + lane % 32, lane / 32);
+    asm("" : "+v"(fbx));
   } else if constexpr (TALL) {
     // the wave's wm-th column block (selected without indexing the bases at
     // run time, which would put them in scratch memory)
@@ -784,7 +791,13 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   auto read_x = [&](auto slot_c, int ks, Frag& f) {
     constexpr int SLOT = decltype(slot_c)::value;
     f.ax = read_a(a_base(slot_c, fax[ks]), a_off(slot_c));
-    f.bx = read_b(fbx, SLOT * GE::B_BYTES + ks * 16 * GE::BROW);
+    if constexpr (BT) {
+      uint32_t b = fbx;
+      if (ks) asm volatile("v_xor_b32 %0, 32, %0" : "+v"(b));   // (at its use: one base stays live)
+      f.bx = read_a(b, SLOT * GE::B_BYTES);
+    } else {
+      f.bx = read_b(fbx, SLOT * GE::B_BYTES + ks * 16 * GE::BROW);
+    }
   };
   auto mma = [&](const Frag& f) {
 #pragma unroll
@@ -931,7 +944,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
       constexpr bool K8 = EPI == kEpiBwd8;
       constexpr int UJ = K8 ? 2 : 1;                  // column blocks of 32 in a unit
       constexpr int UPI = NJ / UJ, UNITS = 2 * UPI;   // units of a row block; of the wave
-      constexpr int kAhead = 2;
+      constexpr int kAhead = TALL ? 1 : 2;            // (registers)
       const int c0 = t.n0 + WCOL * wn;                // the wave's first column
       const int nb = N / kKeepBlock;
       const TileRows dgu_rows(Out, t.row0, t.rows, 4 * N), h_rows(Out2, t.row0, t.rows, 2 * N),
@@ -956,7 +969,65 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
           sc[b][hf] = s_rows.load4(lr * 8 * nb, (r0 * 2 + hf) * nb * 4 + c / kKeepBlock * 4);
         }
       };
-      float sum = 0.f, w = 1.f;
+      float w = 1.f;
+      f32x4 sum;   // <dh, h> of the lane's columns of each block of 32
+      // results of one column block j of 32 (its first column c): a is its dh, gq and uq its g and u
+      auto block = [&](const f32x16& a, uint32_t (&gq)[2][4], uint32_t (&uq)[2][4], const float (&scale)[2], int r0,
+                       int c, bool there, int j) {
+        float part = 0.f;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t pg[2][2], pu[2][2], ph[2][2];   // [4-column group][dword]
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int q4 = 2 * p + q;
+            float g[4], u4[4], dg[4], du[4], h[4];
+            if constexpr (K8) {
+              keep_values4(gq[0][q4], scale[0], g);
+              keep_values4(uq[0][q4], scale[1], u4);
+            } else {
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                keep_values2(gq[v][q4], scale[0], g + 2 * v);
+                keep_values2(uq[v][q4], scale[1], u4 + 2 * v);
+              }
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float dh = a[4 * q4 + v];
+              const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-g[v]));
+              const float silu = g[v] * sg;
+              h[v] = silu * u4[v];
+              part = fmaf(h[v], there ? dh : 0.f, part);
+              const float wdh = w * dh;
+              dg[v] = wdh * u4[v] * (sg + silu * (1.f - sg));
+              du[v] = wdh * silu;
+              h[v] *= w;
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              pg[q][v] = pack_bf16x2(dg[2 * v], dg[2 * v + 1]);
+              pu[q][v] = pack_bf16x2(du[2 * v], du[2 * v + 1]);
+              ph[q][v] = pack_bf16x2(h[2 * v], h[2 * v + 1]);
+            }
+          }
+          asm volatile("" : "+v"(part));   // (summed here: left to the store below, every h stays in a register)
+          const u32x4 vg = eight_columns(pg), vu = eight_columns(pu), vh = eight_columns(ph);
+          if (there) {
+            dgu_rows.store16(vg, dgu_lane, (r0 * 2 * N + c + 16 * p) * 2);
+            dgu_rows.store16(vu, dgu_lane, (r0 * 2 * N + N + c + 16 * p) * 2);
+            h_rows.store16(vh, h_lane, (r0 * N + c + 16 * p) * 2);
+          }
+        }
+        // (the row's other 4-column groups are in lane l + 32)
+        const uint32_t bits = __builtin_bit_cast(uint32_t, part);
+        const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+        const uint32_t lo = sw[0], hi = sw[1];
+        sum[j] = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+      };
+      const int parts = kDotParts * n_tiles;   // of a row; this wave's are 4 consecutive ones
+      const uint32_t dot_lane = lc == 0 ? lr * 4 * parts : kOutOfRange;
+      const int dot_first = kDotParts * (t.n0 / BNO) + 4 * wn;
       auto unit = [&](auto u_c) {
         constexpr int u = decltype(u_c)::value;
         constexpr int i = u / UPI, j0 = (u % UPI) * UJ, b = u % (kAhead + 1);
@@ -964,13 +1035,11 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
         if constexpr (u + kAhead < UNITS) fetch(std::integral_constant<int, u + kAhead>{});
         const int r0 = 64 * wm + 32 * i;
         if constexpr (u % UPI == 0) {
-          sum = 0.f;
           if (row_w) w = TileRows(row_w, t.row0, t.rows, 4).load4(lr * 4, r0 * 4);
         }
 #pragma unroll
         for (int jj = 0; jj < UJ; ++jj) {
           const int j = j0 + jj;
-          const bool there = c0 + 32 * j < N;   // (wave-uniform)
           uint32_t gq[2][4], uq[2][4];          // 8 bits: [0]; 16: the two dwords of 4 columns
           if constexpr (K8) {
             from_halves(raw[b][0][jj], gq[0]);
@@ -982,65 +1051,44 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
               from_quarters(raw[b][1][v], uq, 2 * v);
             }
           }
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            uint32_t pg[2][2], pu[2][2], ph[2][2];   // [4-column group][dword]
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int q4 = 2 * p + q;
-              float g[4], u4[4], dg[4], du[4], h[4];
-              if constexpr (K8) {
-                keep_values4(gq[0][q4], sc[b][0], g);
-                keep_values4(uq[0][q4], sc[b][1], u4);
-              } else {
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                  keep_values2(gq[v][q4], sc[b][0], g + 2 * v);
-                  keep_values2(uq[v][q4], sc[b][1], u4 + 2 * v);
-                }
-              }
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const float dh = acc[j][i][4 * q4 + v];
-                const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-g[v]));
-                const float silu = g[v] * sg;
-                h[v] = silu * u4[v];
-                sum = fmaf(h[v], there ? dh : 0.f, sum);
-                const float wdh = w * dh;
-                dg[v] = wdh * u4[v] * (sg + silu * (1.f - sg));
-                du[v] = wdh * silu;
-                h[v] *= w;
-              }
-#pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                pg[q][v] = pack_bf16x2(dg[2 * v], dg[2 * v + 1]);
-                pu[q][v] = pack_bf16x2(du[2 * v], du[2 * v + 1]);
-                ph[q][v] = pack_bf16x2(h[2 * v], h[2 * v + 1]);
-              }
-            }
-            asm volatile("" : "+v"(sum));   // (summed here: left to the store below, every h stays in a register)
-            const u32x4 vg = eight_columns(pg), vu = eight_columns(pu), vh = eight_columns(ph);
-            if (there) {
-              const int c = c0 + 32 * j + 16 * p;
-              dgu_rows.store16(vg, dgu_lane, (r0 * 2 * N + c) * 2);
-              dgu_rows.store16(vu, dgu_lane, (r0 * 2 * N + N + c) * 2);
-              h_rows.store16(vh, h_lane, (r0 * N + c) * 2);
-            }
-          }
+          block(acc[j][i], gq, uq, sc[b], r0, c0 + 32 * j, c0 + 32 * j < N, j);
         }
         if constexpr (u % UPI == UPI - 1) {
-          if (Part) {
-            // <dh, h> over the wave's columns: the row's other 4-column groups are in lane l + 32
-            const uint32_t bits = __builtin_bit_cast(uint32_t, sum);
-            const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
-            const uint32_t lo = sw[0], hi = sw[1];
-            const int parts = 2 * n_tiles;
-            TileRows(Part, t.row0, t.rows, 4 * parts)
-                .store4(__builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi),
-                        lc == 0 ? lr * 4 * parts : kOutOfRange, (r0 * parts + 2 * (t.n0 / BNO) + wn) * 4);
-          }
+          if (Part) TileRows(Part, t.row0, t.rows, 4 * parts).store16(__builtin_bit_cast(u32x4, sum), dot_lane, (r0 * parts + dot_first) * 4);
         }
       };
+      // (the extra rows first: their accumulators are then free)
+      if constexpr (TALL) {
+        const int c = c0 + 32 * wm;   // the extra rows' column block of this wave
+        if (t.rows > BM && c < N) {   // (wave-uniform)
+          u32x4 xr[2][2];
+          float xs[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int v = 0; v < (K8 ? 1 : 2); ++v)
+              xr[hf][v] = gu_rows.load16(gu_lane, K8 ? BM * 2 * N + hf * N + c : (BM * 2 * N + hf * N + c + 16 * v) * 2);
+            xs[hf] = s_rows.load4(lr * 8 * nb, (BM * 2 + hf) * nb * 4 + c / kKeepBlock * 4);
+          }
+          if (row_w) w = TileRows(row_w, t.row0, t.rows, 4).load4(lr * 4, BM * 4);
+          uint32_t gq[2][4], uq[2][4];
+          if constexpr (K8) {
+            from_halves(xr[0][0], gq[0]);
+            from_halves(xr[1][0], uq[0]);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              from_quarters(xr[0][v], gq, 2 * v);
+              from_quarters(xr[1][v], uq, 2 * v);
+            }
+          }
+          block(acc_x, gq, uq, xs, BM, c, true, 0);
+          if (Part)
+            TileRows(Part, t.row0, t.rows, 4 * parts).store4(sum[0], dot_lane, (BM * parts + dot_first + wm) * 4);
+        } else if (t.rows > BM && Part) {
+          TileRows(Part, t.row0, t.rows, 4 * parts).store4(0.f, dot_lane, (BM * parts + dot_first + wm) * 4);
+        }
+      }
       if (64 * wm < t.rows) {   // (wave-uniform, as below)
         fetch(std::integral_constant<int, 0>{});
         if constexpr (kAhead > 1) fetch(std::integral_constant<int, 1>{});
@@ -1070,6 +1118,16 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
           for (int q4 = 0; q4 < 4; ++q4) {
             const f32x4 v = {acc[j][i][4 * q4], acc[j][i][4 * q4 + 1], acc[j][i][4 * q4 + 2], acc[j][i][4 * q4 + 3]};
             rows.store16(__builtin_bit_cast(u32x4, v), lr * 4 * N + 4 * lc, (r0 * N + c + 8 * q4) * 4);
+          }
+        }
+      }
+      if constexpr (TALL) {
+        const int c = t.n0 + WCOL * wn + 32 * wm;   // the extra rows' column block of this wave
+        if (t.rows > BM && c < N) {   // (wave-uniform)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const f32x4 v = {acc_x[4 * q4], acc_x[4 * q4 + 1], acc_x[4 * q4 + 2], acc_x[4 * q4 + 3]};
+            rows.store16(__builtin_bit_cast(u32x4, v), lr * 4 * N + 4 * lc, (BM * N + c + 8 * q4) * 4);
           }
         }
       }
@@ -1243,7 +1301,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
           }
       }
     }
-    if constexpr (TALL) {
+    if constexpr (TALL && EPI < kEpiKeep8) {
       // the extra rows: acc_x holds row BM + lane % 32, the wave's wm-th
       // column block
       const int r = BM + lr;
@@ -1974,6 +2032,11 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                              a_rows, out2, aux, 1, nullptr, sched, nullptr, wtiled);
   }
+  if constexpr (EPI >= kEpiBwd8 || (EPI == kEpiPlain && BT)) {
+    if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E))
+      return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
+                                                             a_rows, out2, aux, 1, part, sched, row_w, wtiled, kept);
+  }
   if (big_tiles(max_rows, E, K))
     return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                      a_rows, out2, aux, 1, part, sched, row_w, wtiled, kept);
@@ -2093,7 +2156,7 @@ hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_off
                                         nullptr, nullptr, sched, nullptr, true, false, nullptr, kept);
 }
 
-int64_t dot_parts(int I) { return 2 * ceil_div(I, 256); }
+int64_t dot_parts(int I) { return kDotParts * ceil_div(I, 256); }
 
 hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                                 const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
