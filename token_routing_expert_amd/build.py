@@ -26,7 +26,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_debug.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "grouped_ffn.hip", "combine.hip", "wgrad.hip",
-           "api_serving.hip", "quantize.hip", "fp8_ffn.hip", "few.hip", "api_training.hip", "train.hip"]
+           "api_serving.hip", "quantize.hip", "fp8_ffn.hip", "few.hip", "api_training.hip", "train.hip",
+           "small_f32.hip"]
 ARCH = "gfx950"
 
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -49,17 +49,23 @@ bool sizes_positive(int64_t rows, int32_t d, int32_t E, int32_t I, moe_dtype dt)
 }
 
 // What the two products of a forward use beside their operands: h, float32's
-// pre-activations before they are rounded, and (bf16) the down projection's
-// partial sums and the products' tile counters.
+// pre-activations before they are rounded (bf16: those of a few rows), and (bf16)
+// the down projection's float32 rows in ranges (y_split of them; 0: it writes bf16 rows at once), its
+// split tail and the products' tile counters.
 struct FfnLayout {
-  size_t h, gu, split, sched, total;
+  size_t h, gu, extra, y, split, sched, total;
+  int y_split;
 };
 
-FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt) {
+FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt, bool rows32) {
   FfnLayout L;
   size_t o = 0;
+  L.y_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)I, (int)d) : 0;
+  if (!rows32 && L.y_split == 1) L.y_split = 0;
   L.h = o;     o += align256((size_t)(rows * I) * elem_size(dt));
   L.gu = o;    o += dt == MOE_F32 ? align256((size_t)(rows * 2 * I) * 4) : 0;
+  L.extra = o; o += dt == MOE_BF16 ? align256((size_t)keep_extra_floats(rows, (int)E, (int)d, (int)I) * 4) : 0;
+  L.y = o;     o += align256((size_t)(L.y_split * rows * d) * 4);
   L.split = o; o += dt == MOE_BF16 ? align256(split_workspace(rows, (int)E, (int)d, (int)I)) : 0;
   L.sched = o; o += dt == MOE_BF16 ? align256(kSchedWords * 4) : 0;
   L.total = o;
@@ -67,7 +73,7 @@ FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt
 }
 
 struct LayerLayout {
-  size_t perm_ws, row_w, x_perm, y, ffn, total;
+  size_t perm_ws, x_perm, y, ffn, total;
 };
 
 LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, moe_dtype dt) {
@@ -75,10 +81,9 @@ LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, 
   LayerLayout L;
   size_t o = 0;
   L.perm_ws = o; o += permute_index_workspace(P, (int)E);
-  L.row_w = o;   o += dt == MOE_BF16 && k == 1 ? align256((size_t)P * 4) : 0;
   L.x_perm = o;  o += dt == MOE_F32 ? align256((size_t)(P * d) * 4) : 0;   // bf16 gathers rows in place
-  L.y = o;       o += align256((size_t)(P * d) * elem_size(dt));
-  L.ffn = o;     o += ffn_layout(P, d, E, I, dt).total;
+  L.y = o;       o += dt == MOE_F32 ? align256((size_t)(P * d) * 4) : 0;   // bf16: among the products'
+  L.ffn = o;     o += ffn_layout(P, d, E, I, dt, true).total;
   L.total = o;
   return L;
 }
@@ -86,33 +91,44 @@ LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, 
 // The gradients of grouped rows: h and dgu (times the rows' weights), g | u
 // where they are computed again (float32, or bf16's 16-bit codes and their
 // scales), float32's dh.
+// (dx: bf16 rows' dx as float32 ranges, dx_split of them; 0: the product writes
+// bf16 rows at once)
 struct GradLayout {
-  size_t h, dgu, gu, gu_s, dh, total;
+  size_t h, dgu, gu, gu_s, extra, dh, dx, total;
+  int dx_split;
 };
 
-GradLayout grad_layout(int64_t rows, int64_t I, moe_dtype dt, bool again) {
+GradLayout grad_layout(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt, bool layer) {
   const size_t s = elem_size(dt);
+  const bool again = !layer;
   GradLayout L;
+  L.dx_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)(2 * I), (int)d) : layer ? 1 : 0;
+  if (!layer && L.dx_split == 1) L.dx_split = 0;
   size_t o = 0;
   L.h = o;   o += align256((size_t)(rows * I) * s);
   L.dgu = o; o += align256((size_t)(rows * 2 * I) * s);
   L.gu = o;  o += again ? align256((size_t)(rows * 2 * I) * s) : 0;
   L.gu_s = o; o += again && dt == MOE_BF16 ? align256((size_t)(rows * 2 * (I / kKeepBlock)) * 4) : 0;
+  L.extra = o;
+  o += again && dt == MOE_BF16 ? align256((size_t)keep_extra_floats(rows, (int)E, (int)d, (int)I) * 4) : 0;
   L.dh = o;  o += dt == MOE_F32 ? align256((size_t)(rows * I) * 4) : 0;
+  L.dx = o;  o += align256((size_t)(L.dx_split * rows * d) * 4);
   L.total = o;
   return L;
 }
 
-// The layer's backward around them: the rows' weights, the dot products' parts
-// and the rows' dx (float32: a token's sum is rounded once), and the grouped rows
-// of x and dout.
+// The layer's backward around them: the rows' weights, the dot products' parts,
+// and the grouped rows of x and dout.
 struct BackwardLayout {
-  size_t x_perm, dout_perm, row_w, dot, dx_perm, grad, total;
+  size_t x_perm, dout_perm, row_w, dot, grad, total;
 };
 
-int64_t dot_columns(int64_t I, moe_dtype dt) { return dt == MOE_F32 ? 1 : dot_parts((int)I); }
+int64_t dot_columns(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt) {
+  if (dt == MOE_BF16) return dot_parts((int)I);
+  return small_f32(rows, (int)E, (int)d, (int)I) ? I / 32 : 1;
+}
 
-BackwardLayout backward_layout(int64_t T, int64_t d, int64_t k, int64_t I, moe_dtype dt) {
+BackwardLayout backward_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, moe_dtype dt) {
   const int64_t P = T * k;
   const size_t copy = align256((size_t)(P * d) * elem_size(dt));
   BackwardLayout L;
@@ -120,9 +136,8 @@ BackwardLayout backward_layout(int64_t T, int64_t d, int64_t k, int64_t I, moe_d
   L.x_perm = o;    o += copy;
   L.dout_perm = o; o += copy;
   L.row_w = o;     o += align256((size_t)P * 4);
-  L.dot = o;       o += align256((size_t)(P * dot_columns(I, dt)) * 4);
-  L.dx_perm = o;   o += align256((size_t)(P * d) * 4);
-  L.grad = o;      o += grad_layout(P, I, dt, false).total;
+  L.dot = o;       o += align256((size_t)(P * dot_columns(P, E, d, I, dt)) * 4);
+  L.grad = o;      o += grad_layout(P, E, d, I, dt, true).total;
   L.total = o;
   return L;
 }
@@ -143,6 +158,9 @@ moe_status grad_rows_f32(const float* x, const float* dy, const float* row_w, co
                          hipStream_t s) {
   const bool again = kept.q == nullptr;
   float *h = (float*)(ws + L.h), *dgu = (float*)(ws + L.dgu), *gu = (float*)(ws + L.gu), *dh = (float*)(ws + L.dh);
+  if (small_f32(rows, E, d, I))
+    return from_hip(launch_small_grads_f32(x, dy, offs, rows, E, d, I, wgu, wd, kept, row_w, dgu, h, dot, dx,
+                                           dw_gate_up, dw_down, s));
   if (again) TRY(from_hip(launch_gate_up_save_f32(x, offs, rows, E, d, I, wgu, h, gu, s)));
   TRY(from_hip(launch_down_dgrad_f32(dy, offs, rows, E, d, I, wd, dh, s)));
   TRY(from_hip(launch_swiglu_bwd_f32(dh, again ? gu : nullptr, kept, row_w, offs, E, rows, I, dgu, h, dot, s)));
@@ -157,7 +175,7 @@ extern "C" {
 
 size_t moe_grouped_ffn_train_workspace_size(int32_t max_rows, int32_t E, int32_t d, int32_t I, moe_dtype dt) {
   if (!sizes_positive(max_rows, d, E, I, dt)) return 0;
-  return ffn_layout(max_rows, d, E, I, dt).total;
+  return ffn_layout(max_rows, d, E, I, dt, false).total;
 }
 
 moe_status moe_grouped_ffn_train(const void* x_perm, const int32_t* expert_offsets, int32_t max_rows, int32_t E,
@@ -168,30 +186,42 @@ moe_status moe_grouped_ffn_train(const void* x_perm, const int32_t* expert_offse
   if (max_rows == 0) return MOE_OK;
   if (!x_perm || !expert_offsets || !w_gate_up || !w_down || !y_perm || !gu_q || !gu_s) return MOE_ERR_ARG;
   if (!aligned16(x_perm, w_gate_up, w_down, y_perm, gu_q, workspace)) return MOE_ERR_ARG;
-  const FfnLayout L = ffn_layout(max_rows, d, E, I, dt);
+  const FfnLayout L = ffn_layout(max_rows, d, E, I, dt, false);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   char* ws = (char*)workspace;
-  const Kept kept{(int8_t*)gu_q, gu_s};
+  const Kept kept{(int8_t*)gu_q, gu_s, (float*)(ws + L.extra)};
   hipStream_t s = (hipStream_t)stream;
   if (dt == MOE_F32) {
     float *h = (float*)(ws + L.h), *gu = (float*)(ws + L.gu);
+    if (small_f32(max_rows, E, d, I)) {
+      TRY(from_hip(launch_small_gate_up_f32((const float*)x_perm, 0, nullptr, expert_offsets, max_rows, E, d, I,
+                                            (const float*)w_gate_up, h, kept, s)));
+      return from_hip(launch_small_down_f32(h, expert_offsets, max_rows, E, d, I, (const float*)w_down,
+                                            (float*)y_perm, s));
+    }
     TRY(from_hip(launch_gate_up_save_f32((const float*)x_perm, expert_offsets, max_rows, E, d, I,
                                          (const float*)w_gate_up, h, gu, s)));
     TRY(from_hip(launch_keep8_f32(gu, expert_offsets, E, max_rows, I, kept, s)));
     return from_hip(launch_down_f32(h, expert_offsets, max_rows, E, d, I, (const float*)w_down, (float*)y_perm, s));
   }
-  int32_t* sched = (int32_t*)(ws + L.sched);
+  int32_t* sched = claims_tiles(max_rows, E, d, I) ? (int32_t*)(ws + L.sched) : nullptr;
   bf16_t* h = (bf16_t*)(ws + L.h);
-  TRY(from_hip(launch_sched_reset(sched, s)));
+  if (sched) TRY(from_hip(launch_sched_reset(sched, s)));
   TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x_perm, expert_offsets, max_rows, E, d, I,
                                          (const bf16_t*)w_gate_up, h, kept, s, nullptr, 0, sched)));
+  if (L.y_split) {
+    float* y = (float*)(ws + L.y);
+    TRY(from_hip(launch_down_rows32(h, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_down, y, L.y_split, s,
+                                    nullptr, nullptr)));
+    return from_hip(launch_split_sum(y, L.y_split, expert_offsets, E, max_rows, d, (bf16_t*)y_perm, s));
+  }
   return from_hip(launch_down_bf16(h, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_down, (bf16_t*)y_perm, s,
                                    (float*)(ws + L.split), sched));
 }
 
 size_t moe_grouped_ffn_backward_workspace_size(int32_t max_rows, int32_t E, int32_t d, int32_t I, moe_dtype dt) {
   if (!sizes_positive(max_rows, d, E, I, dt)) return 0;
-  return grad_layout(max_rows, I, dt, true).total;
+  return grad_layout(max_rows, E, d, I, dt, false).total;
 }
 
 moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_offsets, int32_t max_rows, int32_t E,
@@ -206,10 +236,10 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
   if (!x_perm || !expert_offsets || !w_gate_up || !w_down || !dy_perm || !dx_perm || !dw_gate_up || !dw_down)
     return MOE_ERR_ARG;
   if (!aligned16(x_perm, w_gate_up, w_down, dy_perm, dx_perm, dw_gate_up, dw_down, gu_q, workspace)) return MOE_ERR_ARG;
-  const GradLayout L = grad_layout(max_rows, I, dt, true);
+  const GradLayout L = grad_layout(max_rows, E, d, I, dt, false);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   char* ws = (char*)workspace;
-  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s, nullptr};
   if (dt == MOE_F32)
     return grad_rows_f32((const float*)x_perm, (const float*)dy_perm, nullptr, expert_offsets, max_rows, E, d, I,
                          (const float*)w_gate_up, (const float*)w_down, kept, (float*)dx_perm, (float*)dw_gate_up,
@@ -217,12 +247,18 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
   const bf16_t *x = (const bf16_t*)x_perm, *dy = (const bf16_t*)dy_perm, *wgu = (const bf16_t*)w_gate_up,
                *wd = (const bf16_t*)w_down;
   bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
-  const Kept again{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s)};
+  const Kept again{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s), (float*)(ws + L.extra)};
   if (!gu_q)
     TRY(from_hip(launch_gate_up_keep16_bf16(x, expert_offsets, max_rows, E, d, I, wgu, again, s, nullptr)));
   TRY(from_hip(launch_down_bwd_bf16(dy, expert_offsets, max_rows, E, d, I, wd, gu_q ? kept : again, gu_q ? 8 : 16,
                                     nullptr, dgu, h, nullptr, s)));
-  TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, expert_offsets, max_rows, E, d, I, wgu, (bf16_t*)dx_perm, s)));
+  if (L.dx_split) {
+    float* dx = (float*)(ws + L.dx);
+    TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, max_rows, E, d, I, wgu, dx, L.dx_split, s)));
+    TRY(from_hip(launch_split_sum(dx, L.dx_split, expert_offsets, E, max_rows, d, (bf16_t*)dx_perm, s)));
+  } else {
+    TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, expert_offsets, max_rows, E, d, I, wgu, (bf16_t*)dx_perm, s)));
+  }
   return from_hip(launch_ffn_wgrad_bf16(x, dy, h, dgu, expert_offsets, max_rows, E, d, I,
                                         (bf16_t*)dw_gate_up, (bf16_t*)dw_down, s));
 }
@@ -247,13 +283,20 @@ moe_status moe_forward_train_q8(const void* x, const float* logits, int32_t T, i
   const LayerLayout L = layer_layout(T, d, E, k, I, dt);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   const int64_t P = (int64_t)T * k;
-  const FfnLayout F = ffn_layout(P, d, E, I, dt);
+  const FfnLayout F = ffn_layout(P, d, E, I, dt, true);
   char *ws = (char*)workspace, *fws = ws + L.ffn;
-  const Kept kept{(int8_t*)gu_q, gu_s};
+  const Kept kept{(int8_t*)gu_q, gu_s, (float*)(fws + F.extra)};
   hipStream_t s = (hipStream_t)stream;
   if (logits) TRY(from_hip(launch_route_topk(logits, T, E, k, topk_idx, topk_w, s)));
   if (dt == MOE_F32) {
     float *xp = (float*)(ws + L.x_perm), *h = (float*)(fws + F.h), *gu = (float*)(fws + F.gu), *y = (float*)(ws + L.y);
+    if (small_f32(P, E, d, I)) {
+      TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s)));
+      TRY(from_hip(launch_small_gate_up_f32((const float*)x, T, row_token, expert_offsets, P, E, d, I,
+                                            (const float*)w_gate_up, h, kept, s)));
+      TRY(from_hip(launch_small_down_f32(h, expert_offsets, P, E, d, I, (const float*)w_down, y, s)));
+      return from_hip(launch_combine_f32(y, P, pair_row, topk_w, T, k, d, (float*)out, s));
+    }
     TRY(from_hip(launch_permute_rows(topk_idx, T, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s,
                                      nullptr, x, (int64_t)d * 4, xp)));
     TRY(from_hip(launch_gate_up_save_f32(xp, expert_offsets, P, E, d, I, (const float*)w_gate_up, h, gu, s)));
@@ -261,31 +304,21 @@ moe_status moe_forward_train_q8(const void* x, const float* logits, int32_t T, i
     TRY(from_hip(launch_down_f32(h, expert_offsets, P, E, d, I, (const float*)w_down, y, s)));
     return from_hip(launch_combine_f32(y, P, pair_row, topk_w, T, k, d, (float*)out, s));
   }
-  // as moe_forward: rows gathered in the products' loads, and with one pair a
-  // token the down projection writes the output rows itself where its tiles allow
+  // rows gathered in the products' loads; y stays float32 until the output's one rounding
   int32_t* sched = (int32_t*)(fws + F.sched);
   bf16_t* h = (bf16_t*)(fws + F.h);
-  float* split = (float*)(fws + F.split);
-  const bool scatter = k == 1 && down_scatters(P, E, d, I, true);
-  float* row_w = scatter ? (float*)(ws + L.row_w) : nullptr;
-  TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s, sched,
-                                    scatter ? topk_w : nullptr, row_w)));
-  if (scatter) TRY(from_hip(launch_zero_unrouted_bf16(pair_row, P, T, d, (bf16_t*)out, s)));
+  float* y = (float*)(fws + F.y);
+  TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s, sched)));
   TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x, expert_offsets, P, E, d, I, (const bf16_t*)w_gate_up, h,
                                          kept, s, row_token, T, sched)));
-  if (scatter) {
-    const DownScatter sc{(bf16_t*)out, row_token, row_w, T};
-    return from_hip(launch_down_bf16(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, nullptr, s, split, sched,
-                                     &sc));
-  }
-  bf16_t* y = (bf16_t*)(ws + L.y);
-  TRY(from_hip(launch_down_bf16(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, y, s, split, sched)));
-  return from_hip(launch_combine_bf16(y, P, pair_row, topk_w, T, k, d, (bf16_t*)out, s));
+  TRY(from_hip(launch_down_rows32(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, y, F.y_split, s,
+                                  (float*)(fws + F.split), sched)));
+  return from_hip(launch_combine_rows32(y, F.y_split, P, pair_row, topk_w, T, k, d, (bf16_t*)out, s));
 }
 
 size_t moe_backward_q8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt) {
   if (!sizes_positive(T, d, E, I, dt) || k < 1) return 0;
-  return backward_layout(T, d, k, I, dt).total;
+  return backward_layout(T, d, E, k, I, dt).total;
 }
 
 moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32_t k, int32_t I,
@@ -302,16 +335,17 @@ moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32
       !gu_s || !dout || !dx || !dw_gate_up || !dw_down || !dtopk_w)
     return MOE_ERR_ARG;
   if (!aligned16(x, w_gate_up, w_down, gu_q, dout, dx, dw_gate_up, dw_down, workspace)) return MOE_ERR_ARG;
-  const BackwardLayout L = backward_layout(T, d, k, I, dt);
+  const BackwardLayout L = backward_layout(T, d, E, k, I, dt);
   if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   const int64_t P = (int64_t)T * k;
   char* ws = (char*)workspace;
   float *row_w = (float*)(ws + L.row_w), *dot = (float*)(ws + L.dot);
-  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s, nullptr};
   // the combine's backward puts w_p before dout; it is applied to h and [dg | du] instead, so that dout stays exact
-  const GradLayout G = grad_layout(P, I, dt, false);
+  // (a token's rows of dx stay float32 until its sum's one rounding)
+  const GradLayout G = grad_layout(P, E, d, I, dt, true);
   char* gws = ws + L.grad;
-  float* dxp = (float*)(ws + L.dx_perm);
+  float* dxp = (float*)(gws + G.dx);
   void *x_perm = ws + L.x_perm, *dout_perm = ws + L.dout_perm;
   TRY(from_hip(launch_pair_rows(x, dout, T, k, (int64_t)d * elem_size(dt), pair_row, topk_w, P, x_perm, dout_perm,
                                 row_w, s)));
@@ -319,17 +353,17 @@ moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32
     TRY(grad_rows_f32((const float*)x_perm, (const float*)dout_perm, row_w, expert_offsets, P, E, d, I,
                       (const float*)w_gate_up, (const float*)w_down, kept, dxp, (float*)dw_gate_up, (float*)dw_down,
                       dot, gws, G, s));
-    return from_hip(launch_combine_grad_f32(dxp, dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
+    return from_hip(launch_combine_grad_f32(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
                                             (float*)dx, dtopk_w, dlogits, s));
   }
   const bf16_t *xp = (const bf16_t*)x_perm, *dyp = (const bf16_t*)dout_perm, *wgu = (const bf16_t*)w_gate_up,
                *wd = (const bf16_t*)w_down;
   bf16_t *h = (bf16_t*)(gws + G.h), *dgu = (bf16_t*)(gws + G.dgu);
   TRY(from_hip(launch_down_bwd_bf16(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, s)));
-  TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, s)));
+  TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, G.dx_split, s)));
   TRY(from_hip(launch_ffn_wgrad_bf16(xp, dyp, h, dgu, expert_offsets, P, E, d, I, (bf16_t*)dw_gate_up,
                                      (bf16_t*)dw_down, s)));
-  return from_hip(launch_combine_grad_bf16(dxp, dot, dot_columns(I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
+  return from_hip(launch_combine_grad_bf16(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
                                            (bf16_t*)dx, dtopk_w, dlogits, s));
 }
 
@@ -340,7 +374,7 @@ moe_status moe_checkpoint_values(const void* gu_q, const float* gu_s, int32_t ro
   if ((int64_t)rows * 2 * I >= kMaxElems) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!gu_q || !gu_s || !gu || !aligned16(gu_q, gu)) return MOE_ERR_ARG;
-  const Kept kept{(int8_t*)gu_q, (float*)gu_s};
+  const Kept kept{(int8_t*)gu_q, (float*)gu_s, nullptr};
   hipStream_t s = (hipStream_t)stream;
   if (dt == MOE_BF16) return from_hip(launch_keep8_values_bf16(kept, rows, I, (bf16_t*)gu, s));
   return from_hip(launch_keep8_values_f32(kept, rows, I, (float*)gu, s));

@@ -73,11 +73,13 @@ __device__ __forceinline__ void store_vec(bf16_t* out, const float* f) {
 // select), for two vectors at a time, so 2 KS gathers are in flight together.
 // Every expert row is read once: non-temporal loads (measured: the cold
 // combine of the 128-expert layer 47.5 -> 45.3 us).
-// (Elem: the rows' type; Out: the output's, which may be narrower.)
-template <typename Elem, int KS, typename Out = Elem>
+// (Elem: the rows' type; Out: the output's, which may be narrower.  SPLIT: y is
+// the sum of n_split arrays of max_rows rows, one behind the other.)
+template <typename Elem, int KS, typename Out = Elem, bool SPLIT = false>
 __device__ __forceinline__ void combine_token(const u32x4* __restrict__ y, int64_t max_rows,
                                               const int32_t* __restrict__ pair_row, const float* __restrict__ pair_w,
-                                              int64_t t, int k, int64_t vec_per_row, Out* __restrict__ out) {
+                                              int64_t t, int k, int64_t vec_per_row, Out* __restrict__ out,
+                                              int n_split = 1) {
   constexpr int n = Vec<Elem>::n;
   const int lane = threadIdx.x % kWave;
   int64_t row[KS];
@@ -92,32 +94,75 @@ __device__ __forceinline__ void combine_token(const u32x4* __restrict__ y, int64
     wt[j] = (j < k && pair_w) ? pair_w[t * k + j] : 1.f;
   }
   for (int64_t v0 = lane; v0 < vec_per_row; v0 += 2 * kWave) {
-    u32x4 g[2][KS];
+    float acc[2][n];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t v = v0 + h * kWave;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < KS; ++j)
-        if (j < k && max_rows > 0 && v < vec_per_row) g[h][j] = __builtin_nontemporal_load(&y[row[j] * vec_per_row + v]);
+      for (int i = 0; i < n; ++i) acc[h][i] = 0.f;
+    for (int sp = 0; sp < (SPLIT ? n_split : 1); ++sp) {
+      const u32x4* ys = y + (SPLIT ? sp * max_rows * vec_per_row : 0);
+      u32x4 g[2][KS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t v = v0 + h * kWave;
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+          if (j < k && max_rows > 0 && v < vec_per_row)
+            g[h][j] = __builtin_nontemporal_load(&ys[row[j] * vec_per_row + v]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          if (j >= k || !live[j]) continue;
+          float f[n];
+          Vec<Elem>::load(g[h][j], f);
+#pragma unroll
+          for (int i = 0; i < n; ++i) acc[h][i] = fmaf(wt[j], f[i], acc[h][i]);
+        }
+      }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t v = v0 + h * kWave;
-      if (v >= vec_per_row) continue;
-      float acc[n];
-#pragma unroll
-      for (int i = 0; i < n; ++i) acc[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        if (j >= k || !live[j]) continue;
-        float f[n];
-        Vec<Elem>::load(g[h][j], f);
-#pragma unroll
-        for (int i = 0; i < n; ++i) acc[i] = fmaf(wt[j], f[i], acc[i]);
-      }
-      store_vec<n>(out + (t * vec_per_row + v) * n, acc);
+      if (v < vec_per_row) store_vec<n>(out + (t * vec_per_row + v) * n, acc[h]);
     }
   }
+}
+
+// Any k, one slot at a time.
+template <typename Out>
+__device__ __forceinline__ void combine_slots(const u32x4* __restrict__ y, int n_split, int64_t max_rows,
+                                              const int32_t* __restrict__ pair_row, const float* __restrict__ pair_w,
+                                              int64_t t, int k, int64_t vec_per_row, Out* __restrict__ out) {
+  for (int64_t v = threadIdx.x % kWave; v < vec_per_row; v += kWave) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int sp = 0; sp < n_split; ++sp)
+      for (int j = 0; j < k; ++j) {
+        const int64_t r = pair_row[t * k + j];
+        if (r < 0 || r >= max_rows) continue;
+        const float w = pair_w ? pair_w[t * k + j] : 1.f;
+        float f[4];
+        Vec<float>::load(y[(sp * max_rows + r) * vec_per_row + v], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      }
+    store_vec<4>(out + (t * vec_per_row + v) * 4, acc);
+  }
+}
+
+// out[t] as k_combine's, from float32 rows in n_split ranges, rounded once.
+template <int KS>
+__global__ __launch_bounds__(kThreads) void k_combine_rows32(const u32x4* __restrict__ y, int n_split,
+                                                             int64_t max_rows, const int32_t* __restrict__ pair_row,
+                                                             const float* __restrict__ pair_w, int64_t n_tok, int k,
+                                                             int64_t vec_per_row, bf16_t* __restrict__ out) {
+  const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
+  if (t >= n_tok) return;
+  if constexpr (KS > 0)
+    combine_token<float, KS, bf16_t, true>(y, max_rows, pair_row, pair_w, t, k, vec_per_row, out, n_split);
+  else
+    combine_slots(y, n_split, max_rows, pair_row, pair_w, t, k, vec_per_row, out);
 }
 
 // KS > 0: at most KS slots (combine_token); KS == 0: any k, one slot at a time
@@ -213,7 +258,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_bwd(
 // KS > 0: at most KS slots; KS == 0: any k, one slot at a time
 template <typename Elem, int KS>
 __global__ __launch_bounds__(kThreads) void k_combine_grad(
-    const u32x4* __restrict__ dx_perm, const float* __restrict__ dot, int64_t n_parts, int64_t max_rows,
+    const u32x4* __restrict__ dx_perm, int n_split, const float* __restrict__ dot, int64_t n_parts, int64_t max_rows,
     const int32_t* __restrict__ pair_row, const float* __restrict__ pair_w, const int32_t* __restrict__ topk_idx,
     int64_t n_tok, int k, int E, int64_t vec_per_row, Elem* __restrict__ dx, float* __restrict__ dw,
     float* __restrict__ dlogits) {
@@ -223,22 +268,10 @@ __global__ __launch_bounds__(kThreads) void k_combine_grad(
   const int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave;
   if (t >= n_tok) return;
   const int lane = threadIdx.x % kWave;
-  if constexpr (KS > 0) {
-    combine_token<float, KS, Elem>(dx_perm, max_rows, pair_row, nullptr, t, k, vec_per_row, dx);
-  } else {
-    for (int64_t v = lane; v < vec_per_row; v += kWave) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < k; ++j) {
-        const int64_t r = pair_row[t * k + j];
-        if (r < 0 || r >= max_rows) continue;
-        float f[4];
-        Vec<float>::load(dx_perm[r * vec_per_row + v], f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += f[i];
-      }
-      store_vec<4>(dx + (t * vec_per_row + v) * 4, acc);
-    }
-  }
+  if constexpr (KS > 0)
+    combine_token<float, KS, Elem, true>(dx_perm, max_rows, pair_row, nullptr, t, k, vec_per_row, dx, n_split);
+  else
+    combine_slots(dx_perm, n_split, max_rows, pair_row, nullptr, t, k, vec_per_row, dx);
   float* my_dw = s_dw[threadIdx.x / kWave];
   float inner = 0.f;
   for (int j = 0; j < k; ++j) {
@@ -341,30 +374,40 @@ hipError_t launch_combine_bwd_f32(const float* dout, const float* y_perm, int64_
 namespace {
 
 template <typename Elem>
-hipError_t launch_grad(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+hipError_t launch_grad(const float* dx_perm, int n_split, const float* dot, int64_t n_parts, int64_t max_rows,
                        const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T, int k, int d,
                        int E, Elem* dx, float* dw, float* dlogits, hipStream_t s) {
   const unsigned blocks = (unsigned)ceil_div(T, kThreads / kWave);
   const auto kernel = k <= 4 ? k_combine_grad<Elem, 4> : k <= 8 ? k_combine_grad<Elem, 8> : k_combine_grad<Elem, 0>;
-  kernel<<<blocks, kThreads, 0, s>>>((const u32x4*)dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k,
+  kernel<<<blocks, kThreads, 0, s>>>((const u32x4*)dx_perm, n_split, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k,
                                      E, d / 4, dx, dw, dlogits);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_combine_grad_bf16(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+hipError_t launch_combine_grad_bf16(const float* dx_perm, int n_split, const float* dot, int64_t n_parts,
+                                    int64_t max_rows,
                                     const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                     int k, int d, int E, bf16_t* dx, float* dw, float* dlogits, hipStream_t s) {
-  return launch_grad<bf16_t>(dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
+  return launch_grad<bf16_t>(dx_perm, n_split, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
                              s);
 }
 
-hipError_t launch_combine_grad_f32(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+hipError_t launch_combine_grad_f32(const float* dx_perm, int n_split, const float* dot, int64_t n_parts,
+                                    int64_t max_rows,
                                    const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                    int k, int d, int E, float* dx, float* dw, float* dlogits, hipStream_t s) {
-  return launch_grad<float>(dx_perm, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
+  return launch_grad<float>(dx_perm, n_split, dot, n_parts, max_rows, pair_row, pair_w, topk_idx, T, k, d, E, dx, dw, dlogits,
                             s);
+}
+
+hipError_t launch_combine_rows32(const float* y_perm, int n_split, int64_t max_rows, const int32_t* pair_row,
+                                 const float* pair_w, int64_t T, int k, int d, bf16_t* out, hipStream_t s) {
+  const auto kernel = k <= 4 ? k_combine_rows32<4> : k <= 8 ? k_combine_rows32<8> : k_combine_rows32<0>;
+  kernel<<<(unsigned)ceil_div(T, kThreads / kWave), kThreads, 0, s>>>((const u32x4*)y_perm, n_split, max_rows,
+                                                                      pair_row, pair_w, T, k, d / 4, out);
+  return hipGetLastError();
 }
 
 hipError_t launch_zero_unrouted_bf16(const int32_t* pair_row, int64_t max_rows, int64_t T, int d, bf16_t* out,

@@ -210,6 +210,9 @@ hipError_t launch_permute_rows(const int32_t* pair_expert, int64_t T, int k, int
 constexpr int kSchedDown = 16;
 constexpr int kSchedWords = 32;
 hipError_t launch_sched_reset(int32_t* sched, hipStream_t s);
+// whether a product of the layer's two may have so many tiles (four rounds) that
+// it claims any: otherwise it does without a counter
+bool claims_tiles(int64_t max_rows, int E, int d, int I);
 
 // Grouped SwiGLU feed-forward, as two launches (gate/up + SwiGLU, then down).
 // h: [max_rows, I] of the activation type.
@@ -318,7 +321,9 @@ constexpr int kKeepBlock = 64;   // columns that share a scale
 struct Kept {
   int8_t* q;   // [rows, 2I], of 8 bits (inside a call also of 16)
   float* s;    // [rows, 2, I/64]
+  float* extra = nullptr;   // scratch of the product that writes one: keep_extra_floats()
 };
+int64_t keep_extra_floats(int64_t max_rows, int E, int d, int I);
 // gate/up with SwiGLU that also writes the checkpoint of its rows
 hipError_t launch_gate_up_keep8_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
                                      int I, const bf16_t* w_gate_up, bf16_t* h, const Kept& kept, hipStream_t s,
@@ -350,9 +355,19 @@ hipError_t launch_keep8_values_bf16(const Kept& kept, int64_t rows, int I, bf16_
 hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& kept, const float* row_w,
                                  const int32_t* expert_offsets, int E, int64_t max_rows, int I, float* dgu, float* h,
                                  float* dot, hipStream_t s);
-// launch_gate_up_dgrad_bf16 with float32 rows
+// Products with float32 rows, in n_split ranges of their k-stages ([n_split,
+// max_rows, N], to be added): launch_gate_up_dgrad_bf16 and launch_down_bf16.
+// rows_split: the number of ranges to take for a product of depth K and N columns
+int rows_split(int64_t max_rows, int E, int K, int N);
 hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,
-                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, hipStream_t s);
+                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, int n_split,
+                                       hipStream_t s);
+hipError_t launch_down_rows32(const bf16_t* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                              const bf16_t* w_down, float* y_perm, int n_split, hipStream_t s, float* split_ws,
+                              int32_t* sched);
+// out [max_rows, N] = the sum of the ranges, rounded (rows below offsets[E])
+hipError_t launch_split_sum(const float* part, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows,
+                            int N, bf16_t* out, hipStream_t s);
 // dh [max_rows, I] = dy Wd^T
 hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                                  const float* w_down, float* dh, hipStream_t s);
@@ -360,15 +375,35 @@ hipError_t launch_down_dgrad_f32(const float* dy, const int32_t* expert_offsets,
 hipError_t launch_pair_rows(const void* x, const void* dout, int64_t T, int k, int64_t row_bytes,
                             const int32_t* pair_row, const float* pair_w, int64_t max_rows, void* x_perm,
                             void* dout_perm, float* row_w, hipStream_t s);
-// dx[t] = the sum of the token's rows of dx_perm [max_rows, d] (float32); dw[p] =
+// launch_combine_bf16 of float32 rows in n_split ranges, y_perm [n_split, max_rows, d]
+hipError_t launch_combine_rows32(const float* y_perm, int n_split, int64_t max_rows, const int32_t* pair_row,
+                                 const float* pair_w, int64_t T, int k, int d, bf16_t* out, hipStream_t s);
+// dx[t] = the sum of the token's rows of dx_perm [n_split, max_rows, d] (float32); dw[p] =
 // the sum of its row's n_parts dot products (0 for a pair without a row); dlogits
 // (optional) as launch_combine_bwd_bf16's
-hipError_t launch_combine_grad_bf16(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+hipError_t launch_combine_grad_bf16(const float* dx_perm, int n_split, const float* dot, int64_t n_parts, int64_t max_rows,
                                     const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                     int k, int d, int E, bf16_t* dx, float* dw, float* dlogits, hipStream_t s);
-hipError_t launch_combine_grad_f32(const float* dx_perm, const float* dot, int64_t n_parts, int64_t max_rows,
+hipError_t launch_combine_grad_f32(const float* dx_perm, int n_split, const float* dot, int64_t n_parts, int64_t max_rows,
                                    const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                    int k, int d, int E, float* dx, float* dw, float* dlogits, hipStream_t s);
+
+// ---- float32 products of few tiles (small_f32.hip) ----
+// whether a training call's float32 products take them
+bool small_f32(int64_t max_rows, int E, int d, int I);
+// h and the checkpoint; with row_token, row r's x is row row_token[r] of x [x_rows, d]
+hipError_t launch_small_gate_up_f32(const float* x, int64_t x_rows, const int32_t* row_token,
+                                    const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                    const float* w_gate_up, float* h, const Kept& kept, hipStream_t s);
+hipError_t launch_small_down_f32(const float* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 const float* w_down, float* y, hipStream_t s);
+// every gradient of grouped rows, from the checkpoint or, where kept.q is null,
+// from g | u computed again; dgu [max_rows, 2I] and h [max_rows, I] are scratch;
+// row_w and dot ([max_rows, I / 32] parts) as launch_down_bwd_bf16's
+hipError_t launch_small_grads_f32(const float* x, const float* dy, const int32_t* expert_offsets, int64_t max_rows,
+                                  int E, int d, int I, const float* w_gate_up, const float* w_down, const Kept& kept,
+                                  const float* row_w, float* dgu, float* h, float* dot, float* dx, float* dw_gate_up,
+                                  float* dw_down, hipStream_t s);
 
 // ---- 8-bit codes and scales (quantize.hip) ----
 // rows and expert weights to e4m3 with a float32 scale for each block of 128

@@ -70,7 +70,8 @@ constexpr int kEpiKeep8 = 6;       // as kEpiSwiglu, and the checkpoint of [A Wg
 constexpr int kEpiKeep16 = 7;      // the checkpoint in 16-bit codes, nothing else
 constexpr int kEpiBwd8 = 8;        // Out = w [dg | du] (row stride 2N), Out2 = w h from dh = A W and the checkpoint
 constexpr int kEpiBwd16 = 9;       // as kEpiBwd8 from 16-bit codes
-constexpr int kEpiRows32 = 10;     // Part = A W (float32, row stride N)
+constexpr int kEpiRows32 = 10;     // (float*)Out[split] = A W over the split's k-stages (float32, row stride N)
+constexpr int kTallRows = 256, kTallExtra = 32;   // rows of a tall tile: of its first part, and past it
 constexpr int kDotParts = 8;       // dot products of a row that a column tile of kEpiBwd8 writes, one for 32 columns
 constexpr int kBwdBlocks = 1;      // column blocks whose g, u the backward epilogue loads together
 
@@ -233,9 +234,9 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     const bf16_t* __restrict__ W, bf16_t* __restrict__ Out, int n_tiles, const int32_t* __restrict__ row_token,
     int64_t a_rows, bf16_t* __restrict__ Out2, const bf16_t* __restrict__ Aux, int n_split_arg,
     float* __restrict__ Part, int32_t* __restrict__ sched, const float* __restrict__ row_w, int wtiled, Kept kept) {
-  // (k-split ranges are only used with the lockstep tiles: the ping-pong
-  // instances see one range per tile, a constant)
-  const int n_split = PP ? 1 : n_split_arg;
+  // (k-split ranges are used with the lockstep tiles and, but for tall tiles,
+  // float32 rows: the other ping-pong instances see one range per tile, a constant)
+  const int n_split = PP && (EPI != kEpiRows32 || TL) ? 1 : n_split_arg;
   // gate/up tiles: 128 gate columns and the matching 128 up columns
   constexpr bool SWIGLU = is_gate_up(EPI);
   static_assert(!(SWIGLU && BT), "the gate/up weight is only read as [K][2N]");
@@ -248,6 +249,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   static_assert(BT || (SWIGLU ? BNB == 2 * kTileGateCols : BNB == kTileDownCols),
                 "column-tiled weights are blocked for the products' tile width");
   static_assert(BM <= 256, "one index DMA covers 256 rows");
+  static_assert(!TL || BM == kTallRows, "tall tiles are 256-row ones");
   static_assert(!PP || WAVES == 8, "ping-pong pairs two groups of four waves, one wave of each per SIMD");
   // With kEpiScatter the tile's row -> token map (and row weights) serve
   // the epilogue, not the activation loads: the activations are the
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   constexpr bool SCATTER = EPI == kEpiScatter;
   static_assert(!SCATTER || WAVES >= 2, "the row weights are fetched by wave 1");
   constexpr int NSLOT = SCATTER ? 4 : 2;
-  // Tall tiles (TL: the ping-pong products but those that save pre-activations): an expert's
+  // Tall tiles (TL: the ping-pong products): an expert's
   // last tile also takes up to XR = 32 rows past BM, so that they do not make
   // a tile of their own -- one that would stream the expert's whole weight
   // slice again, and run its whole stage loop, for a few rows.  Waves 0 and 1
@@ -269,9 +271,9 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   // SwiGLU pairs stay in one lane.  The block costs one MFMA per wave and
   // k-step.
   constexpr bool TALL = TL;
-  static_assert(!TL || (PP && (EPI == kEpiPlain || EPI == kEpiSwiglu || EPI >= kEpiBwd8)),
+  static_assert(!TL || (PP && (EPI == kEpiPlain || EPI == kEpiSwiglu || EPI >= kEpiKeep8)),
                 "tall tiles: ping-pong products with an epilogue for the extra rows");
-  constexpr int XR = TALL ? 32 : 0;
+  constexpr int XR = TALL ? kTallExtra : 0;
   constexpr int A_STAGE = GE::A_BYTES + XR * BK * 2;  // LDS bytes of an activation stage
   typedef Geo<2 * BK, NJ, WM> GD;  // the activation geometry of a double-stage
   // Activation double-stages (every ping-pong product; the backward's
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   // tS ranges of k-stages (pieces); a piece writes its float32 partial tile
   // to the workspace, and k_tail_sum adds the pieces of every such tile in
   // order (deterministic) and applies the epilogue.
-  constexpr bool TAIL = PP && !BT && (EPI == kEpiPlain || EPI == kEpiScatter);
+  constexpr bool TAIL = PP && !BT && (EPI == kEpiPlain || EPI == kEpiScatter || EPI == kEpiRows32);
   int tS = 1;
   int64_t t_full = total_tiles, t_exc = 0;
   if (TAIL && Part != nullptr && n_split == 1 && total_tiles > G && total_tiles % G != 0) {
@@ -369,7 +371,8 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
   const int64_t total_units = tS > 1 ? t_full + t_exc * tS : total_tiles * n_split;
   if (vb >= total_units) return;  // the whole workgroup: no barrier follows
   const int my_tiles = (int)((total_units - vb + G - 1) / G);  // units of this workgroup
-  auto k_begin = [&](int split) { return split * nk / n_split; };
+  // (double-stages: every range starts at an even stage)
+  auto k_begin = [&](int split) { return AD ? 2 * (split * (nk / 2) / n_split) : split * nk / n_split; };
   // unit u: its tile, its range of k-stages [k0, k1), and its piece of a
   // split tail tile (-1: a whole tile or an n_split range)
   auto unit_tile = [&](int64_t u) -> int64_t {
@@ -871,6 +874,21 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
       const int c0 = t.n0 + (WCOL / 2) * wn;
       if (c0 >= N) return;   // (wave-uniform)
       constexpr bool K8 = EPI == kEpiKeep8;
+      if constexpr (TALL) {
+        // An extra row's block of 64 columns lies in four waves, 16 columns
+        // each: g and u go out as they are, and k_keep_extra finishes them.
+        // acc_x[4 q4 + v] is gate column 16 wm + 8 q4 + lc + v of the wave's 64 for
+        // q4 < 2 and the matching up column for q4 + 2.
+        if (t.rows > BM) {
+          const TileRows x_rows(kept.extra, (int64_t)t.e * XR, t.rows - BM, 8 * N);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const f32x4 v = {acc_x[4 * q4], acc_x[4 * q4 + 1], acc_x[4 * q4 + 2], acc_x[4 * q4 + 3]};
+            x_rows.store16(__builtin_bit_cast(u32x4, v), lr * 8 * N + 4 * lc,
+                           ((q4 < 2 ? 0 : N) + c0 + 16 * wm + 8 * (q4 % 2)) * 4);
+          }
+        }
+      }
       const int nb = N / kKeepBlock;
       const TileRows q_rows(kept.q, t.row0, t.rows, (K8 ? 2 : 4) * N), s_rows(kept.s, t.row0, t.rows, 8 * nb);
       const uint32_t h_lane = lr * 2 * N + 4 * lc, q_lane = K8 ? h_lane : lr * 4 * N + 4 * lc;
@@ -1105,7 +1123,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
         if (64 * wm + 32 < t.rows) row_block(std::integral_constant<int, 1>{});
       }
     } else if constexpr (EPI == kEpiRows32) {
-      const TileRows rows(Part, t.row0, t.rows, 4 * N);
+      const TileRows rows((const float*)Out + (int64_t)split * max_rows * N, t.row0, t.rows, 4 * N);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r0 = 64 * wm + 32 * i;
@@ -1523,7 +1541,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
     // expert's last rows then finishes with its full sibling on the same
     // weight slice instead of running ahead of it, and the two keep sharing
     // the slice's stages in L2 (measured: the projection 1.4-4.4% faster).
-    constexpr bool kKeepPace = PP && (EPI == kEpiPlain || EPI == kEpiScatter);
+    constexpr bool kKeepPace = PP && (EPI == kEpiPlain || EPI == kEpiScatter || EPI == kEpiRows32);
     const bool active = kKeepPace || 64 * wm < cur.rows;
     cur_tall = TALL && cur.rows > BM;
     int cur_k0, cur_k1;
@@ -1927,7 +1945,9 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
 // rounded to bf16, or with row_token (one pair per token) that times the
 // row's routing weight, rounded again, into its token's row of out.  The
 // header says how many tiles were split (none: every block returns).
+// ROWS32: the row as it is, float32 (out points to floats).
 constexpr int kTailSumRows = 4;
+template <bool ROWS32>
 __global__ __launch_bounds__(256) void k_tail_sum(const float* __restrict__ ws, int N, bf16_t* __restrict__ out,
                                                   const int32_t* __restrict__ row_token,
                                                   const float* __restrict__ row_w, int64_t out_rows) {
@@ -1950,6 +1970,10 @@ __global__ __launch_bounds__(256) void k_tail_sum(const float* __restrict__ ws, 
 #pragma unroll
     for (int pc = 1; pc < kTailMaxSplit; ++pc)
       if (pc < n_pc) sum += p[pc];
+    if constexpr (ROWS32) {
+      *(f32x4*)((float*)out + (row0 + r) * N + n0 + c) = sum;
+      return;
+    }
     const uint2 y = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
     if (!row_token) {
       *(uint2*)(out + (row0 + r) * N + n0 + c) = y;
@@ -2018,9 +2042,9 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
                        const bf16_t* w, bf16_t* out, hipStream_t s, const int32_t* row_token, int64_t a_rows,
                        bf16_t* out2, const bf16_t* aux, int32_t* sched, float* tail_ws, bool allow_tall,
                        bool wtiled, const float* row_w, const Kept& kept) {
-  // (Part: a tail workspace for the down projection, the dot products of the backward's epilogue, float32 rows)
-  constexpr bool kPart = (EPI == kEpiPlain && !BT) || EPI >= kEpiBwd8;
-  constexpr bool kRowPart = kPart && EPI != kEpiPlain;   // (split tails are the 256-row tiles')
+  // (Part: a tail workspace for the down projection, the dot products of the backward's epilogue)
+  constexpr bool kRowPart = EPI == kEpiBwd8 || EPI == kEpiBwd16;   // (split tails are the 256-row tiles')
+  constexpr bool kPart = kRowPart || (EPI == kEpiPlain && !BT);
   float* part = kPart ? tail_ws : nullptr;
   if constexpr (EPI == kEpiPlain && !BT) {
     if (allow_tall && big_tiles(max_rows, E, K) && tall_tiles(max_rows, E) && row_token == nullptr)
@@ -2032,7 +2056,7 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                              a_rows, out2, aux, 1, nullptr, sched, nullptr, wtiled);
   }
-  if constexpr (EPI >= kEpiBwd8 || (EPI == kEpiPlain && BT)) {
+  if constexpr (kRowPart || (EPI == kEpiPlain && BT)) {
     if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E))
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                              a_rows, out2, aux, 1, part, sched, row_w, wtiled, kept);
@@ -2072,6 +2096,13 @@ hipError_t launch_gate_up_bf16(const bf16_t* x, const int32_t* expert_offsets, i
 bool down_tail_possible(int64_t max_rows, int E, int d, int I) {
   const int64_t max_mt = max_rows / 256 + (E < max_rows ? E : max_rows);
   return max_rows > kSplitMaxRows && big_tiles(max_rows, E, I) && max_mt * ceil_div(d, 256) > (int64_t)num_cus();
+}
+
+bool claims_tiles(int64_t max_rows, int E, int d, int I) {
+  const int64_t max_mt = max_rows / 256 + (E < max_rows ? E : max_rows);
+  const int64_t most = ceil_div(I, kTileGateCols) > ceil_div(d, kTileDownCols) ? ceil_div(I, kTileGateCols)
+                                                                               : ceil_div(d, kTileDownCols);
+  return big_tiles(max_rows, E, d < I ? d : I) && max_mt * most >= 4 * (int64_t)num_cus();
 }
 
 size_t split_workspace(int64_t max_rows, int E, int d, int I) {
@@ -2122,7 +2153,7 @@ hipError_t launch_down_bf16(const bf16_t* h, const int32_t* expert_offsets, int6
     e = launch_auto<kEpiPlain, false>(h, expert_offsets, max_rows, E, I, d, d, w_down, y_perm, s, nullptr, 0,
                                       nullptr, nullptr, dn_sched, tail_ws, !scatter_tiles, wtiled);
   if (e != hipSuccess || tail_ws == nullptr) return e;
-  k_tail_sum<<<dim3(kTailPieces / 2, 288 / kTailSumRows), 256, 0, s>>>(
+  k_tail_sum<false><<<dim3(kTailPieces / 2, 288 / kTailSumRows), 256, 0, s>>>(
       tail_ws, d, sc ? sc->out : y_perm, sc ? sc->row_token : nullptr, sc ? sc->row_w : nullptr, sc ? sc->T : 0);
   return hipGetLastError();
 }
@@ -2142,18 +2173,84 @@ hipError_t launch_down_dgrad_swiglu_bf16(const bf16_t* dy, const int32_t* expert
                                           nullptr, gu);
 }
 
+namespace {
+
+// The extra rows of a tall gate/up product (an expert's at most 32 rows past its
+// last 256-row tile) from their float32 g | u in kept.extra [E, 32, 2N]: the
+// checkpoint and, of 8 bits, h.  16 lanes take a row's block of 64 columns.
+template <int BITS>
+__global__ __launch_bounds__(256) void k_keep_extra(const int32_t* __restrict__ offsets, int64_t max_rows, int N,
+                                                    Kept kept, bf16_t* __restrict__ h) {
+  const int e = blockIdx.x, nb = N / kKeepBlock;
+  const int64_t lo = clampi<int64_t>(offsets[e], 0, max_rows);
+  const int cnt = (int)(clampi<int64_t>(offsets[e + 1], lo, max_rows) - lo);
+  const int full = (cnt - 1) / kTallRows;   // (the tile list's rule)
+  const int rows = cnt - full * kTallRows;
+  if (cnt <= kTallRows || rows > kTallExtra) return;
+  const int item = blockIdx.y * 16 + threadIdx.x / 16, l16 = threadIdx.x % 16;
+  const int r = item / nb, b = item % nb;
+  if (r >= rows) return;
+  const int64_t row = lo + (int64_t)full * kTallRows + r;
+  const float* src = kept.extra + ((int64_t)e * kTallExtra + r) * 2 * N + b * kKeepBlock + 4 * l16;
+  f32x4 v[2];
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    v[hf] = *(const f32x4*)(src + hf * N);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[hf][i]));
+    float s, inv;
+    keep_scale<BITS>(max16(m), s, inv);
+    const int64_t at = row * 2 * N + hf * N + b * kKeepBlock + 4 * l16;
+    if constexpr (BITS == 8)
+      *(uint32_t*)(kept.q + at) = keep_codes4(v[hf][0], v[hf][1], v[hf][2], v[hf][3], inv);
+    else
+      *(uint2*)(kept.q + 2 * at) = make_uint2(keep_codes2(v[hf][0], v[hf][1], inv), keep_codes2(v[hf][2], v[hf][3], inv));
+    if (l16 == 0) kept.s[(row * 2 + hf) * nb + b] = s;
+  }
+  if constexpr (BITS == 8) {
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = v[0][i] * __builtin_amdgcn_rcpf(1.f + __expf(-v[0][i])) * v[1][i];
+    *(uint2*)(h + row * N + b * kKeepBlock + 4 * l16) = pack4(f);
+  }
+}
+
+template <int BITS>
+hipError_t launch_keep(const bf16_t* x, const int32_t* offsets, int64_t max_rows, int E, int d, int I, const bf16_t* w,
+                       bf16_t* h, const Kept& kept, hipStream_t s, const int32_t* row_token, int64_t x_rows,
+                       int32_t* sched) {
+  constexpr int EPI = BITS == 8 ? kEpiKeep8 : kEpiKeep16;
+  if (!keep_extra_floats(max_rows, E, d, I))
+    return launch_auto<EPI, false>(x, offsets, max_rows, E, d, I, 2 * I, w, h, s, row_token, x_rows, nullptr, nullptr,
+                                   sched, nullptr, true, false, nullptr, kept);
+  const hipError_t e =
+      launch_dma<EPI, false, 32, 1, 4, 4, 4, true, true>(x, offsets, max_rows, E, d, I, 2 * I, w, h, s, row_token,
+                                                         x_rows, nullptr, nullptr, 1, nullptr, sched, nullptr, false,
+                                                         kept);
+  if (e != hipSuccess) return e;
+  const unsigned blocks = (unsigned)ceil_div((int64_t)kTallExtra * (I / kKeepBlock), 16);
+  k_keep_extra<BITS><<<dim3((unsigned)E, blocks), 256, 0, s>>>(offsets, max_rows, I, kept, h);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t keep_extra_floats(int64_t max_rows, int E, int d, int I) {
+  if (!big_tiles(max_rows, E, d) || !tall_tiles(max_rows, E)) return 0;
+  return (int64_t)E * kTallExtra * 2 * I;
+}
+
 hipError_t launch_gate_up_keep8_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
                                      int I, const bf16_t* w_gate_up, bf16_t* h, const Kept& kept, hipStream_t s,
                                      const int32_t* row_token, int64_t x_rows, int32_t* sched) {
-  return launch_auto<kEpiKeep8, false>(x, expert_offsets, max_rows, E, d, I, 2 * I, w_gate_up, h, s, row_token, x_rows,
-                                       nullptr, nullptr, sched, nullptr, true, false, nullptr, kept);
+  return launch_keep<8>(x, expert_offsets, max_rows, E, d, I, w_gate_up, h, kept, s, row_token, x_rows, sched);
 }
 
 hipError_t launch_gate_up_keep16_bf16(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
                                       int I, const bf16_t* w_gate_up, const Kept& kept, hipStream_t s,
                                       int32_t* sched) {
-  return launch_auto<kEpiKeep16, false>(x, expert_offsets, max_rows, E, d, I, 2 * I, w_gate_up, nullptr, s, nullptr, 0,
-                                        nullptr, nullptr, sched, nullptr, true, false, nullptr, kept);
+  return launch_keep<16>(x, expert_offsets, max_rows, E, d, I, w_gate_up, nullptr, kept, s, nullptr, 0, sched);
 }
 
 int64_t dot_parts(int I) { return kDotParts * ceil_div(I, 256); }
@@ -2169,11 +2266,82 @@ hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets,
                                      nullptr, nullptr, dot, true, false, row_w, kept);
 }
 
+namespace {
+
+// Float32 rows of a product, in n_split ranges of its k-stages: out [n_split,
+// max_rows, N].  tail_ws: as launch_down_bf16's split_ws (one range only).
+template <bool BT>
+hipError_t launch_rows32(const bf16_t* a, const int32_t* offsets, int64_t max_rows, int E, int K, int N, int ldw,
+                         const bf16_t* w, float* out, int n_split, hipStream_t s, float* tail_ws, int32_t* sched) {
+  constexpr int EPI = kEpiRows32;
+  bf16_t* o = (bf16_t*)out;
+  if (big_tiles(max_rows, E, K)) {
+    if (n_split == 1 && tall_tiles(max_rows, E))
+      return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0,
+                                                             nullptr, nullptr, 1, tail_ws, sched);
+    return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr,
+                                                     nullptr, n_split, tail_ws, sched);
+  }
+  if (small_tiles(max_rows, E))
+    return launch_dma<EPI, BT, 32, 2, 4, 1, 3, false>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr,
+                                                      nullptr, n_split);
+  return launch_dma<EPI, BT>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr, nullptr, n_split);
+}
+
+}  // namespace
+
+// Ranges that a product's k-stages are cut into where its tiles are fewer than
+// the places for them: a tile's time is its stages, one after the other, while
+// CUs stand idle.  The split with the least estimated time: rounds of tiles (of
+// even row shares, half a tile lost an expert) times a range's stages at the
+// measured time of a stage, and the float32 ranges written and read again at the
+// rate of a copy.
+int rows_split(int64_t max_rows, int E, int K, int N) {
+  const bool big = big_tiles(max_rows, E, K), small = small_tiles(max_rows, E);
+  const int bm = big ? 256 : small ? 64 : 128;
+  const double stage_us = big ? 0.8 : small ? 0.45 : 0.6;
+  const int64_t slots = (big ? 1 : 2) * (int64_t)num_cus();
+  const int64_t experts = E < max_rows ? E : max_rows;
+  const double tiles = ((double)max_rows / bm + 0.5 * experts) * (double)ceil_div(N, 256);
+  const double range_us = 2.0 * 4 * (double)max_rows * N / 4.8e6;
+  int best = 1;
+  double best_us = 0;
+  for (int sp = 1; sp <= kSplitMax && (sp == 1 || (K / 32) / sp >= 8); ++sp) {
+    const double rounds = (double)(int64_t)((tiles * sp + slots - 1) / slots);
+    const double us = (rounds < 1 ? 1 : rounds) * (K / 32 / sp + 4) * stage_us + sp * range_us;
+    if (sp == 1 || us < 0.8 * best_us) {
+      best = sp;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
 hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,
-                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, hipStream_t s) {
+                                       int d, int I, const bf16_t* w_gate_up, float* dx_perm, int n_split,
+                                       hipStream_t s) {
   // as launch_gate_up_dgrad_bf16
-  return launch_auto<kEpiRows32, true>(dgu, expert_offsets, max_rows, E, 2 * I, d, 2 * I, w_gate_up, nullptr, s,
-                                       nullptr, 0, nullptr, nullptr, nullptr, dx_perm);
+  return launch_rows32<true>(dgu, expert_offsets, max_rows, E, 2 * I, d, 2 * I, w_gate_up, dx_perm, n_split, s,
+                             nullptr, nullptr);
+}
+
+hipError_t launch_down_rows32(const bf16_t* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                              const bf16_t* w_down, float* y_perm, int n_split, hipStream_t s, float* split_ws,
+                              int32_t* sched) {
+  float* tail_ws = n_split == 1 && split_ws && down_tail_possible(max_rows, E, d, I) ? split_ws : nullptr;
+  const hipError_t e = launch_rows32<false>(h, expert_offsets, max_rows, E, I, d, d, w_down, y_perm, n_split, s,
+                                            tail_ws, sched ? sched + kSchedDown : nullptr);
+  if (e != hipSuccess || tail_ws == nullptr) return e;
+  k_tail_sum<true><<<dim3(kTailPieces / 2, 288 / kTailSumRows), 256, 0, s>>>(tail_ws, d, (bf16_t*)y_perm, nullptr,
+                                                                             nullptr, 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_split_sum(const float* part, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows,
+                            int N, bf16_t* out, hipStream_t s) {
+  k_split_sum<<<dim3((unsigned)ceil_div(N / 4, 256), (unsigned)max_rows), 256, 0, s>>>(
+      part, n_split, expert_offsets, E, max_rows, N, out, nullptr, nullptr, 0);
+  return hipGetLastError();
 }
 
 hipError_t launch_gate_up_dgrad_bf16(const bf16_t* dgu, const int32_t* expert_offsets, int64_t max_rows, int E,

@@ -66,6 +66,14 @@ __device__ __forceinline__ void keep_values2(uint32_t codes, float s, float* v) 
   v[1] = fmaf((float)(b >> 16), s, off);
 }
 
+// max over 16 consecutive lanes (quads, then mirrored halves)
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));   // mirror in 8 lanes
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror in 16 lanes
+}
+
 // A row of an MFMA result block: 32 columns in lanes l and l + 32, register q4
 // holding columns 8 q4 + 4 (l / 32) .. +3 as one dword.  to_halves gives lane l
 // the dwords of columns 16 (l / 32) .. +15 in order, from_halves takes them back.

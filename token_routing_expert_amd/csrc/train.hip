@@ -10,14 +10,6 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
 
-// max over 16 consecutive lanes (quads, then mirrored halves)
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));    // lane ^ 1
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));    // lane ^ 2
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, true));   // mirror in 8 lanes
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror in 16 lanes
-}
-
 // 16 lanes take a block of 64, four values each.
 __global__ __launch_bounds__(kThreads) void k_keep8_f32(const float* __restrict__ gu,
                                                         const int32_t* __restrict__ offsets, int E, int64_t max_rows,
