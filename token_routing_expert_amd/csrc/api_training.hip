@@ -49,21 +49,23 @@ bool sizes_positive(int64_t rows, int32_t d, int32_t E, int32_t I, moe_dtype dt)
 }
 
 // What the two products of a forward use beside their operands: h, float32's
-// pre-activations before they are rounded (bf16: those of a few rows), and (bf16)
-// the down projection's float32 rows in ranges (y_split of them; 0: it writes bf16 rows at once), its
+// pre-activations before they are rounded (bf16: those of a few rows, or, where
+// gate/up's k-stages are cut into gu_split > 1 ranges, theirs), and (bf16) the down
+// projection's float32 rows in ranges (y_split of them; 0: it writes bf16 rows at once), its
 // split tail and the products' tile counters.
 struct FfnLayout {
   size_t h, gu, extra, y, split, sched, total;
-  int y_split;
+  int gu_split, y_split;
 };
 
 FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt, bool rows32) {
   FfnLayout L;
   size_t o = 0;
+  L.gu_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 1;
   L.y_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)I, (int)d) : 0;
   if (!rows32 && L.y_split == 1) L.y_split = 0;
   L.h = o;     o += align256((size_t)(rows * I) * elem_size(dt));
-  L.gu = o;    o += dt == MOE_F32 ? align256((size_t)(rows * 2 * I) * 4) : 0;
+  L.gu = o;    o += dt == MOE_F32 || L.gu_split > 1 ? align256((size_t)(L.gu_split * rows * 2 * I) * 4) : 0;
   L.extra = o; o += dt == MOE_BF16 ? align256((size_t)keep_extra_floats(rows, (int)E, (int)d, (int)I) * 4) : 0;
   L.y = o;     o += align256((size_t)(L.y_split * rows * d) * 4);
   L.split = o; o += dt == MOE_BF16 ? align256(split_workspace(rows, (int)E, (int)d, (int)I)) : 0;
@@ -92,16 +94,19 @@ LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, 
 // where they are computed again (float32, or bf16's 16-bit codes and their
 // scales), float32's dh.
 // (dx: bf16 rows' dx as float32 ranges, dx_split of them; 0: the product writes
-// bf16 rows at once)
+// bf16 rows at once; gu32, dh: ranges of bf16's other two products of rows, where
+// they are cut)
 struct GradLayout {
-  size_t h, dgu, gu, gu_s, extra, dh, dx, total;
-  int dx_split;
+  size_t h, dgu, gu, gu_s, extra, gu32, dh, dx, dw, total;
+  int gu_split, dh_split, dx_split, dw_split;   // ranges of the row gradients' k and of the weight gradients' rows
 };
 
 GradLayout grad_layout(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt, bool layer) {
   const size_t s = elem_size(dt);
   const bool again = !layer;
   GradLayout L;
+  L.gu_split = dt == MOE_BF16 && again ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 1;
+  L.dh_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)d, (int)I) : 1;
   L.dx_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)(2 * I), (int)d) : layer ? 1 : 0;
   if (!layer && L.dx_split == 1) L.dx_split = 0;
   size_t o = 0;
@@ -111,8 +116,12 @@ GradLayout grad_layout(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype 
   L.gu_s = o; o += again && dt == MOE_BF16 ? align256((size_t)(rows * 2 * (I / kKeepBlock)) * 4) : 0;
   L.extra = o;
   o += again && dt == MOE_BF16 ? align256((size_t)keep_extra_floats(rows, (int)E, (int)d, (int)I) * 4) : 0;
-  L.dh = o;  o += dt == MOE_F32 ? align256((size_t)(rows * I) * 4) : 0;
+  L.gu32 = o;
+  o += L.gu_split > 1 ? align256((size_t)(L.gu_split * rows * 2 * I) * 4) : 0;
+  L.dh = o;  o += dt == MOE_F32 || L.dh_split > 1 ? align256((size_t)(L.dh_split * rows * I) * 4) : 0;
   L.dx = o;  o += align256((size_t)(L.dx_split * rows * d) * 4);
+  L.dw_split = dt == MOE_BF16 ? ffn_wgrad_split(rows, (int)E, (int)d, (int)I) : 1;
+  L.dw = o;  o += L.dw_split > 1 ? align256((size_t)(L.dw_split * E * 3 * d * I) * 4) : 0;
   L.total = o;
   return L;
 }
@@ -124,7 +133,7 @@ struct BackwardLayout {
 };
 
 int64_t dot_columns(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt) {
-  if (dt == MOE_BF16) return dot_parts((int)I);
+  if (dt == MOE_BF16) return rows_split(rows, (int)E, (int)d, (int)I) > 1 ? 1 : dot_parts((int)I);
   return small_f32(rows, (int)E, (int)d, (int)I) ? I / 32 : 1;
 }
 
@@ -148,6 +157,30 @@ moe_status zero_weight_gradients(int32_t E, int32_t d, int32_t I, moe_dtype dt, 
   const int64_t halves = dt == MOE_F32 ? 2 : 1;   // a float32 element is cleared as two bf16 ones
   TRY(from_hip(launch_zero_bf16((bf16_t*)dw_gate_up, (int64_t)E * d * 2 * I * halves, s)));
   return from_hip(launch_zero_bf16((bf16_t*)dw_down, (int64_t)E * I * d * halves, s));
+}
+
+// The checkpoint (of 8 or 16 bits) of rows x, and of 8 bits h: in one kernel, or,
+// where the product's k-stages are cut into ranges, in gu and from there.
+moe_status gate_up_keep(const bf16_t* x, int64_t x_rows, const int32_t* row_token, const int32_t* offs, int64_t rows,
+                        int32_t E, int32_t d, int32_t I, const bf16_t* wgu, bf16_t* h, const Kept& kept, int bits,
+                        int gu_split, float* gu, hipStream_t s, int32_t* sched) {
+  if (gu_split > 1) {
+    TRY(from_hip(launch_gate_up_rows32(x, offs, rows, E, d, I, wgu, gu, gu_split, s, row_token, x_rows)));
+    return from_hip(launch_keep_rows(gu, gu_split, offs, E, rows, I, kept, bits, h, s));
+  }
+  if (bits == 16) return from_hip(launch_gate_up_keep16_bf16(x, offs, rows, E, d, I, wgu, kept, s, sched));
+  return from_hip(launch_gate_up_keep8_bf16(x, offs, rows, E, d, I, wgu, h, kept, s, row_token, x_rows, sched));
+}
+
+// w [dg | du], w h and the parts of <dh, h> of rows with gradient dy, the same way.
+moe_status down_bwd(const bf16_t* dy, const int32_t* offs, int64_t rows, int32_t E, int32_t d, int32_t I,
+                    const bf16_t* wd, const Kept& kept, int bits, const float* row_w, bf16_t* dgu, bf16_t* h,
+                    float* dot, int dh_split, float* dh, hipStream_t s) {
+  if (dh_split > 1) {
+    TRY(from_hip(launch_down_dgrad_rows32(dy, offs, rows, E, d, I, wd, dh, dh_split, s)));
+    return from_hip(launch_swiglu_bwd_rows(dh, dh_split, kept, bits, row_w, offs, E, rows, I, dgu, h, dot, s));
+  }
+  return from_hip(launch_down_bwd_bf16(dy, offs, rows, E, d, I, wd, kept, bits, row_w, dgu, h, dot, s));
 }
 
 // The gradients of grouped rows x with dy (times row_w), float32: from the
@@ -207,8 +240,8 @@ moe_status moe_grouped_ffn_train(const void* x_perm, const int32_t* expert_offse
   int32_t* sched = claims_tiles(max_rows, E, d, I) ? (int32_t*)(ws + L.sched) : nullptr;
   bf16_t* h = (bf16_t*)(ws + L.h);
   if (sched) TRY(from_hip(launch_sched_reset(sched, s)));
-  TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x_perm, expert_offsets, max_rows, E, d, I,
-                                         (const bf16_t*)w_gate_up, h, kept, s, nullptr, 0, sched)));
+  TRY(gate_up_keep((const bf16_t*)x_perm, 0, nullptr, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_gate_up, h,
+                   kept, 8, L.gu_split, (float*)(ws + L.gu), s, sched));
   if (L.y_split) {
     float* y = (float*)(ws + L.y);
     TRY(from_hip(launch_down_rows32(h, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_down, y, L.y_split, s,
@@ -249,9 +282,10 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
   bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
   const Kept again{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s), (float*)(ws + L.extra)};
   if (!gu_q)
-    TRY(from_hip(launch_gate_up_keep16_bf16(x, expert_offsets, max_rows, E, d, I, wgu, again, s, nullptr)));
-  TRY(from_hip(launch_down_bwd_bf16(dy, expert_offsets, max_rows, E, d, I, wd, gu_q ? kept : again, gu_q ? 8 : 16,
-                                    nullptr, dgu, h, nullptr, s)));
+    TRY(gate_up_keep(x, 0, nullptr, expert_offsets, max_rows, E, d, I, wgu, nullptr, again, 16, L.gu_split,
+                     (float*)(ws + L.gu32), s, nullptr));
+  TRY(down_bwd(dy, expert_offsets, max_rows, E, d, I, wd, gu_q ? kept : again, gu_q ? 8 : 16, nullptr, dgu, h, nullptr,
+               L.dh_split, (float*)(ws + L.dh), s));
   if (L.dx_split) {
     float* dx = (float*)(ws + L.dx);
     TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, max_rows, E, d, I, wgu, dx, L.dx_split, s)));
@@ -260,7 +294,7 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
     TRY(from_hip(launch_gate_up_dgrad_bf16(dgu, expert_offsets, max_rows, E, d, I, wgu, (bf16_t*)dx_perm, s)));
   }
   return from_hip(launch_ffn_wgrad_bf16(x, dy, h, dgu, expert_offsets, max_rows, E, d, I,
-                                        (bf16_t*)dw_gate_up, (bf16_t*)dw_down, s));
+                                        (bf16_t*)dw_gate_up, (bf16_t*)dw_down, L.dw_split, (float*)(ws + L.dw), s));
 }
 
 size_t moe_forward_train_q8_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t I, moe_dtype dt) {
@@ -309,8 +343,8 @@ moe_status moe_forward_train_q8(const void* x, const float* logits, int32_t T, i
   bf16_t* h = (bf16_t*)(fws + F.h);
   float* y = (float*)(fws + F.y);
   TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s, sched)));
-  TRY(from_hip(launch_gate_up_keep8_bf16((const bf16_t*)x, expert_offsets, P, E, d, I, (const bf16_t*)w_gate_up, h,
-                                         kept, s, row_token, T, sched)));
+  TRY(gate_up_keep((const bf16_t*)x, T, row_token, expert_offsets, P, E, d, I, (const bf16_t*)w_gate_up, h, kept, 8,
+                   F.gu_split, (float*)(fws + F.gu), s, sched));
   TRY(from_hip(launch_down_rows32(h, expert_offsets, P, E, d, I, (const bf16_t*)w_down, y, F.y_split, s,
                                   (float*)(fws + F.split), sched)));
   return from_hip(launch_combine_rows32(y, F.y_split, P, pair_row, topk_w, T, k, d, (bf16_t*)out, s));
@@ -359,10 +393,10 @@ moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32
   const bf16_t *xp = (const bf16_t*)x_perm, *dyp = (const bf16_t*)dout_perm, *wgu = (const bf16_t*)w_gate_up,
                *wd = (const bf16_t*)w_down;
   bf16_t *h = (bf16_t*)(gws + G.h), *dgu = (bf16_t*)(gws + G.dgu);
-  TRY(from_hip(launch_down_bwd_bf16(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, s)));
+  TRY(down_bwd(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, G.dh_split, (float*)(gws + G.dh), s));
   TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, G.dx_split, s)));
   TRY(from_hip(launch_ffn_wgrad_bf16(xp, dyp, h, dgu, expert_offsets, P, E, d, I, (bf16_t*)dw_gate_up,
-                                     (bf16_t*)dw_down, s)));
+                                     (bf16_t*)dw_down, G.dw_split, (float*)(gws + G.dw), s)));
   return from_hip(launch_combine_grad_bf16(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
                                            (bf16_t*)dx, dtopk_w, dlogits, s));
 }

@@ -341,10 +341,13 @@ hipError_t launch_down_bwd_bf16(const bf16_t* dy, const int32_t* expert_offsets,
                                 const bf16_t* w_down, const Kept& kept, int bits, const float* row_w, bf16_t* dgu,
                                 bf16_t* h, float* dot, hipStream_t s);
 // dw_down[e] = sum of h^T dy and dw_gate_up[e] = sum of x^T dgu over the rows of
-// expert e, in one launch
+// expert e, in one launch; with ffn_wgrad_split() ranges of rows their float32 sums
+// pass through part [n_split, E, 3 d I] (1: not used)
+constexpr int kWgradSplitMax = 16;
+int ffn_wgrad_split(int64_t max_rows, int E, int d, int I);
 hipError_t launch_ffn_wgrad_bf16(const bf16_t* x, const bf16_t* dy, const bf16_t* h, const bf16_t* dgu,
                                  const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
-                                 bf16_t* dw_gate_up, bf16_t* dw_down, hipStream_t s);
+                                 bf16_t* dw_gate_up, bf16_t* dw_down, int n_split, float* part, hipStream_t s);
 // the checkpoint of gu [rows, 2I] float32 (rows below offsets[E]), and its values
 hipError_t launch_keep8_f32(const float* gu, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
                             const Kept& kept, hipStream_t s);
@@ -365,6 +368,20 @@ hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_
 hipError_t launch_down_rows32(const bf16_t* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
                               const bf16_t* w_down, float* y_perm, int n_split, hipStream_t s, float* split_ws,
                               int32_t* sched);
+// and the two products whose epilogues need whole sums: gu [n_split, max_rows, 2I]
+// and dh [n_split, max_rows, I], finished by launch_keep_rows and launch_swiglu_bwd_rows
+hipError_t launch_gate_up_rows32(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 const bf16_t* w_gate_up, float* gu, int n_split, hipStream_t s,
+                                 const int32_t* row_token, int64_t x_rows);
+hipError_t launch_down_dgrad_rows32(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                    int I, const bf16_t* w_down, float* dh, int n_split, hipStream_t s);
+// the checkpoint (bits: 8 or 16) and, of 8 bits, h of gu's rows
+hipError_t launch_keep_rows(const float* gu, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
+                            const Kept& kept, int bits, bf16_t* h, hipStream_t s);
+// dgu, h and dot [max_rows] as launch_down_bwd_bf16's
+hipError_t launch_swiglu_bwd_rows(const float* dh, int n_split, const Kept& kept, int bits, const float* row_w,
+                                  const int32_t* expert_offsets, int E, int64_t max_rows, int I, bf16_t* dgu,
+                                  bf16_t* h, float* dot, hipStream_t s);
 // out [max_rows, N] = the sum of the ranges, rounded (rows below offsets[E])
 hipError_t launch_split_sum(const float* part, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows,
                             int N, bf16_t* out, hipStream_t s);

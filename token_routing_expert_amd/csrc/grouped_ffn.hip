@@ -2192,28 +2192,8 @@ __global__ __launch_bounds__(256) void k_keep_extra(const int32_t* __restrict__ 
   if (r >= rows) return;
   const int64_t row = lo + (int64_t)full * kTallRows + r;
   const float* src = kept.extra + ((int64_t)e * kTallExtra + r) * 2 * N + b * kKeepBlock + 4 * l16;
-  f32x4 v[2];
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    v[hf] = *(const f32x4*)(src + hf * N);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[hf][i]));
-    float s, inv;
-    keep_scale<BITS>(max16(m), s, inv);
-    const int64_t at = row * 2 * N + hf * N + b * kKeepBlock + 4 * l16;
-    if constexpr (BITS == 8)
-      *(uint32_t*)(kept.q + at) = keep_codes4(v[hf][0], v[hf][1], v[hf][2], v[hf][3], inv);
-    else
-      *(uint2*)(kept.q + 2 * at) = make_uint2(keep_codes2(v[hf][0], v[hf][1], inv), keep_codes2(v[hf][2], v[hf][3], inv));
-    if (l16 == 0) kept.s[(row * 2 + hf) * nb + b] = s;
-  }
-  if constexpr (BITS == 8) {
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = v[0][i] * __builtin_amdgcn_rcpf(1.f + __expf(-v[0][i])) * v[1][i];
-    *(uint2*)(h + row * N + b * kKeepBlock + 4 * l16) = pack4(f);
-  }
+  const f32x4 v[2] = {*(const f32x4*)src, *(const f32x4*)(src + N)};
+  keep_block<BITS>(v, row, b * kKeepBlock + 4 * l16, N, l16, kept, h);
 }
 
 template <int BITS>
@@ -2272,20 +2252,21 @@ namespace {
 // max_rows, N].  tail_ws: as launch_down_bf16's split_ws (one range only).
 template <bool BT>
 hipError_t launch_rows32(const bf16_t* a, const int32_t* offsets, int64_t max_rows, int E, int K, int N, int ldw,
-                         const bf16_t* w, float* out, int n_split, hipStream_t s, float* tail_ws, int32_t* sched) {
+                         const bf16_t* w, float* out, int n_split, hipStream_t s, float* tail_ws, int32_t* sched,
+                         const int32_t* row_token = nullptr, int64_t a_rows = 0) {
   constexpr int EPI = kEpiRows32;
   bf16_t* o = (bf16_t*)out;
   if (big_tiles(max_rows, E, K)) {
     if (n_split == 1 && tall_tiles(max_rows, E))
-      return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0,
+      return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows,
                                                              nullptr, nullptr, 1, tail_ws, sched);
-    return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr,
+    return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows, nullptr,
                                                      nullptr, n_split, tail_ws, sched);
   }
   if (small_tiles(max_rows, E))
-    return launch_dma<EPI, BT, 32, 2, 4, 1, 3, false>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr,
+    return launch_dma<EPI, BT, 32, 2, 4, 1, 3, false>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows, nullptr,
                                                       nullptr, n_split);
-  return launch_dma<EPI, BT>(a, offsets, max_rows, E, K, N, ldw, w, o, s, nullptr, 0, nullptr, nullptr, n_split);
+  return launch_dma<EPI, BT>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows, nullptr, nullptr, n_split);
 }
 
 }  // namespace
@@ -2295,7 +2276,10 @@ hipError_t launch_rows32(const bf16_t* a, const int32_t* offsets, int64_t max_ro
 // CUs stand idle.  The split with the least estimated time: rounds of tiles (of
 // even row shares, half a tile lost an expert) times a range's stages at the
 // measured time of a stage, and the float32 ranges written and read again at the
-// rate of a copy.
+// rate of a copy.  All three products of a backward that computes g | u again, cut
+// and not: 16 rows, 1 expert, 2560 x 64: 45 and 100 us; 345 rows, 5 experts,
+// 2880 x 1024: 112 and 190; 256 rows, 16 experts, 2048 x 768: 116 and 141; the same
+// times (none is cut) from 2192 rows, 2 experts, 1408 x 1472 on.
 int rows_split(int64_t max_rows, int E, int K, int N) {
   const bool big = big_tiles(max_rows, E, K), small = small_tiles(max_rows, E);
   const int bm = big ? 256 : small ? 64 : 128;
@@ -2308,7 +2292,8 @@ int rows_split(int64_t max_rows, int E, int K, int N) {
   double best_us = 0;
   for (int sp = 1; sp <= kSplitMax && (sp == 1 || (K / 32) / sp >= 8); ++sp) {
     const double rounds = (double)(int64_t)((tiles * sp + slots - 1) / slots);
-    const double us = (rounds < 1 ? 1 : rounds) * (K / 32 / sp + 4) * stage_us + sp * range_us;
+    // (ranges are added by a pass of their own or in a pass that would else read one: 6 us)
+    const double us = (rounds < 1 ? 1 : rounds) * (K / 32 / sp + 4) * stage_us + sp * range_us + (sp > 1 ? 6 : 0);
     if (sp == 1 || us < 0.8 * best_us) {
       best = sp;
       best_us = us;
@@ -2323,6 +2308,18 @@ hipError_t launch_gate_up_dgrad_rows32(const bf16_t* dgu, const int32_t* expert_
   // as launch_gate_up_dgrad_bf16
   return launch_rows32<true>(dgu, expert_offsets, max_rows, E, 2 * I, d, 2 * I, w_gate_up, dx_perm, n_split, s,
                              nullptr, nullptr);
+}
+
+hipError_t launch_gate_up_rows32(const bf16_t* x, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                                 const bf16_t* w_gate_up, float* gu, int n_split, hipStream_t s,
+                                 const int32_t* row_token, int64_t x_rows) {
+  return launch_rows32<false>(x, expert_offsets, max_rows, E, d, 2 * I, 2 * I, w_gate_up, gu, n_split, s, nullptr,
+                              nullptr, row_token, x_rows);
+}
+
+hipError_t launch_down_dgrad_rows32(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                                    int I, const bf16_t* w_down, float* dh, int n_split, hipStream_t s) {
+  return launch_rows32<true>(dy, expert_offsets, max_rows, E, d, I, d, w_down, dh, n_split, s, nullptr, nullptr);
 }
 
 hipError_t launch_down_rows32(const bf16_t* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,

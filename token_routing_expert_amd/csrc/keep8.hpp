@@ -74,6 +74,33 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, true));  // mirror in 16 lanes
 }
 
+// One block of a row's checkpoint by 16 lanes, four columns each (v[0] its gates,
+// v[1] its ups, at column c of I): codes and scales, and of 8 bits h in bf16.
+template <int BITS>
+__device__ __forceinline__ void keep_block(const f32x4 (&v)[2], int64_t row, int c, int I, int l16, const Kept& kept,
+                                           bf16_t* __restrict__ h) {
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[hf][i]));
+    float s, inv;
+    keep_scale<BITS>(max16(m), s, inv);
+    const int64_t at = (row * 2 + hf) * I + c;
+    if constexpr (BITS == 8)
+      *(uint32_t*)(kept.q + at) = keep_codes4(v[hf][0], v[hf][1], v[hf][2], v[hf][3], inv);
+    else
+      *(uint2*)(kept.q + 2 * at) = make_uint2(keep_codes2(v[hf][0], v[hf][1], inv), keep_codes2(v[hf][2], v[hf][3], inv));
+    if (l16 == 0) kept.s[(row * 2 + hf) * (I / kKeepBlock) + c / kKeepBlock] = s;
+  }
+  if constexpr (BITS == 8) {
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = v[0][i] * __builtin_amdgcn_rcpf(1.f + __expf(-v[0][i])) * v[1][i];
+    *(uint2*)(h + row * I + c) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  }
+}
+
 // A row of an MFMA result block: 32 columns in lanes l and l + 32, register q4
 // holding columns 8 q4 + 4 (l / 32) .. +3 as one dword.  to_halves gives lane l
 // the dwords of columns 16 (l / 32) .. +15 in order, from_halves takes them back.

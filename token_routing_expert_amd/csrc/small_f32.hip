@@ -13,7 +13,7 @@
 // What such a call costs is its launches and one memory round trip each, so the
 // steps are few: the SwiGLU backward sits behind dh (with g | u computed again
 // beside it where there is no checkpoint), and dx and both weight gradients, which
-// do not read one another, are one launch.  Measured: see launch_small_* below.
+// do not read one another, are one launch.  Measured: at small_f32 below.
 #include "keep8.hpp"
 
 #include <algorithm>
@@ -331,16 +331,20 @@ unsigned row_tiles(int64_t max_rows, int E) { return (unsigned)(max_rows / kRows
 
 }  // namespace
 
-// Few tiles of 64 x 128, and few rows an expert: a weight gradient's tile walks
-// all of an expert's rows.  Measured (one step of moe_grouped_ffn_train and
+// Few tiles of 64 x 128, and few rows an expert (more of them where the tiles are
+// fewest): a weight gradient's tile walks all of an expert's rows.  Measured (one step of moe_grouped_ffn_train and
 // moe_grouped_ffn_backward, this way and with the 64 x 128 tiles, us): 128 rows, 8
 // experts, 128 x 256: 31 and 70; 512, 16, 512 x 512: 83 and 153; 64, 16, 1024 x
 // 1024: 201 and 332; 1024, 8, 512 x 1024: 228 and 264; above, 2048, 16, 512 x 512:
 // 222 and 204; 2000, 2, 704 x 320: 272 and 221; 1000, 1, 1024 x 1024: 369 and 329.
+// Of more than 128 rows an expert: 264, 2, 640 x 704: 81 and 181; 512, 1, 1024 x
+// 512: 158 and 218; 1500, 3, 128 x 1024: 144 and 227; 2000, 8, 128 x 128: 61 and 83.
 bool small_f32(int64_t max_rows, int E, int d, int I) {
   const int64_t tiles = max_rows / 64 + std::min<int64_t>(E, max_rows);
   const int width = d < I ? d : I;
-  return max_rows <= 128 * (int64_t)E && tiles * ceil_div(width, 128) <= 160 && (int64_t)E * d * I <= ((int64_t)1 << 24);
+  const int64_t t = tiles * ceil_div(width, 128);
+  return ((max_rows <= 128 * (int64_t)E && t <= 160) || (max_rows <= 512 * (int64_t)E && t <= 64)) &&
+         (int64_t)E * d * I <= ((int64_t)1 << 24);
 }
 
 hipError_t launch_small_gate_up_f32(const float* x, int64_t x_rows, const int32_t* row_token,

@@ -94,6 +94,77 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd_f32(const float* __rest
   if (lane == 0) dot[r] = sum;
 }
 
+// The sum of n_split ranges' four elements at p, `stride` floats apart.
+__device__ __forceinline__ f32x4 add_ranges(const float* __restrict__ p, int n_split, int64_t stride) {
+  f32x4 sum = *(const f32x4*)p;
+  for (int sp = 1; sp < n_split; ++sp) sum += *(const f32x4*)(p + sp * stride);
+  return sum;
+}
+
+// 16 lanes take a row's block of 64 gates and ups.
+template <int BITS>
+__global__ __launch_bounds__(kThreads) void k_keep_rows(const float* __restrict__ gu, int n_split,
+                                                        const int32_t* __restrict__ offsets, int E, int64_t max_rows,
+                                                        int I, Kept kept, bf16_t* __restrict__ h) {
+  const int nb = I / kKeepBlock;
+  const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 16;
+  const int64_t row = item / nb;
+  if (row >= clampi<int64_t>(offsets[E], 0, max_rows)) return;   // (the same for 16 lanes)
+  const int l16 = threadIdx.x % 16, c = (int)(item - row * nb) * kKeepBlock + 4 * l16;
+  const float* p = gu + row * 2 * I + c;
+  const f32x4 v[2] = {add_ranges(p, n_split, max_rows * 2 * I), add_ranges(p + I, n_split, max_rows * 2 * I)};
+  keep_block<BITS>(v, row, c, I, l16, kept, h);
+}
+
+// One wave a grouped row, four columns a lane: the bf16 products' SwiGLU backward
+// (grouped_ffn.hip, kEpiBwd8) of whole sums.
+template <int BITS>
+__global__ __launch_bounds__(kThreads) void k_swiglu_bwd_rows(const float* __restrict__ dh, int n_split, Kept kept,
+                                                              const float* __restrict__ row_w,
+                                                              const int32_t* __restrict__ offsets, int E,
+                                                              int64_t max_rows, int I, bf16_t* __restrict__ dgu,
+                                                              bf16_t* __restrict__ h, float* __restrict__ dot) {
+  const int64_t r = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
+  if (r >= clampi<int64_t>(offsets[E], 0, max_rows)) return;
+  const int lane = threadIdx.x % kWave, nb = I / kKeepBlock;
+  const float w = row_w ? row_w[r] : 1.f;
+  float sum = 0.f;
+  for (int c = 4 * lane; c < I; c += 4 * kWave) {
+    float v[2][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int64_t at = (r * 2 + hf) * I + c;
+      const float s = kept.s[(r * 2 + hf) * nb + c / kKeepBlock];
+      if constexpr (BITS == 8) {
+        keep_values4(*(const uint32_t*)(kept.q + at), s, v[hf]);
+      } else {
+        const uint2 q = *(const uint2*)(kept.q + 2 * at);
+        keep_values2(q.x, s, v[hf]);
+        keep_values2(q.y, s, v[hf] + 2);
+      }
+    }
+    const f32x4 d = add_ranges(dh + r * I + c, n_split, max_rows * I);
+    float dg[4], du[4], hv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float g = v[0][i], u = v[1][i];
+      const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-g)), silu = g * sg, wdh = w * d[i];
+      hv[i] = silu * u;
+      sum = fmaf(hv[i], d[i], sum);
+      dg[i] = wdh * u * (sg + silu * (1.f - sg));
+      du[i] = wdh * silu;
+      hv[i] *= w;
+    }
+    *(uint2*)(dgu + r * 2 * I + c) = make_uint2(pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+    *(uint2*)(dgu + r * 2 * I + I + c) = make_uint2(pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
+    *(uint2*)(h + r * I + c) = make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
+  }
+  if (!dot) return;
+#pragma unroll
+  for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  if (lane == 0) dot[r] = sum;
+}
+
 // One wave a token: its rows of x and dout to every grouped row its pairs have,
 // and those rows' routing weights.
 __global__ __launch_bounds__(kThreads) void k_pair_rows(const u32x4* __restrict__ x, const u32x4* __restrict__ dout,
@@ -169,6 +240,23 @@ hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& k
   else
     k_swiglu_bwd_f32<true><<<blocks, kThreads, 0, s>>>(dh, gu, kept, row_w, expert_offsets, E, max_rows, I, dgu, h,
                                                        dot);
+  return hipGetLastError();
+}
+
+hipError_t launch_keep_rows(const float* gu, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
+                            const Kept& kept, int bits, bf16_t* h, hipStream_t s) {
+  const unsigned blocks = blocks_of(max_rows * (I / kKeepBlock), kThreads / 16);
+  const auto kernel = bits == 16 ? k_keep_rows<16> : k_keep_rows<8>;
+  kernel<<<blocks, kThreads, 0, s>>>(gu, n_split, expert_offsets, E, max_rows, I, kept, h);
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd_rows(const float* dh, int n_split, const Kept& kept, int bits, const float* row_w,
+                                  const int32_t* expert_offsets, int E, int64_t max_rows, int I, bf16_t* dgu,
+                                  bf16_t* h, float* dot, hipStream_t s) {
+  const auto kernel = bits == 16 ? k_swiglu_bwd_rows<16> : k_swiglu_bwd_rows<8>;
+  kernel<<<blocks_of(max_rows, kWaves), kThreads, 0, s>>>(dh, n_split, kept, row_w, expert_offsets, E, max_rows, I, dgu,
+                                                          h, dot);
   return hipGetLastError();
 }
 

@@ -42,19 +42,24 @@ __device__ __forceinline__ uint32_t tile_byte(int kr, int c) {
   return (uint32_t)(kr * ROWB + ((c ^ ((kr & 3) << 2)) << 4));
 }
 
-// One gradient dW = A^T B of every expert, in m_tiles x n_tiles tiles.
+// One gradient dW = A^T B of every expert, in m_tiles x n_tiles tiles (part: its
+// float32 partial sums, [n_split, E, M, N]).
 struct Job {
   const bf16_t *a, *b;
   bf16_t* dw;
   int lda, M, ldb, N, m_tiles, n_tiles;
+  float* part;
 };
 
 // JOBS gradients in one launch: an expert's tiles of the first, then of the
 // second.  (Gathering token rows here instead of reading grouped copies was 35%
 // slower, 3.4 ms on the 128-expert layer where the two copies take 0.08.)
-template <int JOBS>
+// SPLIT: where tiles are few and rows many, an expert's stages of rows are cut
+// into n_split ranges, each a tile of its own, whose float32 sums k_wgrad_sum adds.
+template <int JOBS, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void k_wgrad(Job job0, Job job1, const int32_t* __restrict__ offsets,
-                                                  int64_t max_rows, int E) {
+                                                  int64_t max_rows, int E, int n_split_arg) {
+  const int n_split = SPLIT ? n_split_arg : 1;
   constexpr int AROW = kBM * 2, BROW = kBN * 2;                 // bytes per k-row of a stage
   constexpr int A_BYTES = kBK * AROW, B_BYTES = kBK * BROW;     // 8 KB and 16 KB
   constexpr int A_RPI = 1024 / AROW, B_RPI = 1024 / BROW;       // k-rows per 1 KB load
@@ -79,11 +84,11 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(Job job0, Job job1, const int3
   // round-robin.
   const int G = gridDim.x, W = G / kXcd;
   const int xcd = blockIdx.x % kXcd, local = blockIdx.x / kXcd;
-  const int per_job = job0.m_tiles * job0.n_tiles;
-  const int per_e = per_job + (JOBS > 1 ? job1.m_tiles * job1.n_tiles : 0);
+  const int per_job = job0.m_tiles * job0.n_tiles * n_split;
+  const int per_e = per_job + (JOBS > 1 ? job1.m_tiles * job1.n_tiles * n_split : 0);
   const int n_all = E * per_e;
   struct Tile {
-    int e, m0, n0, lo, cnt, ns;
+    int e, m0, n0, lo, cnt, ns, split;
     bool second;
   };
   auto job_of = [&](const Tile& t) -> const Job& { return JOBS > 1 && t.second ? job1 : job0; };
@@ -107,12 +112,20 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(Job job0, Job job1, const int3
     int rem = vb - t.e * per_e;
     t.second = JOBS > 1 && rem >= per_job;
     if (t.second) rem -= per_job;
+    t.split = rem % n_split;
+    rem /= n_split;
     const int m_tiles = job_of(t).m_tiles;
     t.m0 = (rem % m_tiles) * kBM;
     t.n0 = (rem / m_tiles) * kBN;
     t.lo = pick(lo4, t.e);
     t.cnt = pick(cnt4, t.e);
     t.ns = (t.cnt + kBK - 1) / kBK;
+    if constexpr (SPLIT) {
+      const int k0 = (int)((int64_t)t.ns * t.split / n_split), k1 = (int)((int64_t)t.ns * (t.split + 1) / n_split);
+      t.lo += k0 * kBK;
+      t.cnt = min(t.cnt - k0 * kBK, (k1 - k0) * kBK);
+      t.ns = k1 - k0;
+    }
     return t;
   };
   // the range [v_lo, v_hi) of this XCD: lane j sums the stages of experts
@@ -280,6 +293,23 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(Job job0, Job job1, const int3
     const int slot = (g + kNS - 1) % kNS;
     char* blk = wave < 2 ? sA + slot * A_BYTES + wave * 4096 : sB + slot * B_BYTES + (wave - 2) * 4096;
     const int M = job_of(t).M, N = job_of(t).N;
+    if constexpr (SPLIT) {
+      float* part = job_of(t).part + ((int64_t)t.split * E + t.e) * M * N;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = t.m0 + 64 * wm + 32 * i + lane % 32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int n = t.n0 + 128 * wn + 32 * j + 8 * q4 + 4 * (lane / 32);
+            if (m < M && n < N)
+              *(f32x4*)(part + (int64_t)m * N + n) =
+                  f32x4{acc[j][i][4 * q4], acc[j][i][4 * q4 + 1], acc[j][i][4 * q4 + 2], acc[j][i][4 * q4 + 3]};
+          }
+      }
+      continue;
+    }
     bf16_t* out = job_of(t).dw + (int64_t)t.e * M * N;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -312,6 +342,19 @@ __global__ __launch_bounds__(256, 2) void k_wgrad(Job job0, Job job1, const int3
   }
 }
 
+// The sums of the ranges of both gradients, rounded: four elements a thread.
+__global__ __launch_bounds__(256) void k_wgrad_sum(Job job0, Job job1, int E, int n_split) {
+  const int64_t n0 = (int64_t)E * job0.M * job0.N, n = n0 + (int64_t)E * job1.M * job1.N;
+  for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < n; i += 4 * (int64_t)gridDim.x * 256) {
+    const bool second = i >= n0;
+    const Job& J = second ? job1 : job0;
+    const int64_t at = second ? i - n0 : i, stride = second ? n - n0 : n0;
+    f32x4 sum = *(const f32x4*)(J.part + at);
+    for (int sp = 1; sp < n_split; ++sp) sum += *(const f32x4*)(J.part + sp * stride + at);
+    *(uint2*)(J.dw + at) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+  }
+}
+
 // CUs of the current device (256 if the query fails)
 int device_cus() {
   int dev = 0, n = 0;
@@ -340,7 +383,7 @@ hipError_t launch_zero_bf16(bf16_t* p, int64_t n, hipStream_t s) {
 namespace {
 
 Job make_job(const bf16_t* a, int lda, int M, const bf16_t* b, int ldb, int N, bf16_t* dw) {
-  return {a, b, dw, lda, M, ldb, N, (int)ceil_div(M, kBM), (int)ceil_div(N, kBN)};
+  return {a, b, dw, lda, M, ldb, N, (int)ceil_div(M, kBM), (int)ceil_div(N, kBN), nullptr};
 }
 
 // persistent: two workgroups per CU at most, a multiple of the XCD count
@@ -359,18 +402,52 @@ hipError_t launch_wgrad_bf16(const bf16_t* a, int lda, int M, const bf16_t* b, i
   const Job job = make_job(a, lda, M, b, ldb, N, dw);
   const unsigned grid = grid_of((int64_t)E * job.m_tiles * job.n_tiles);
   if (grid == 0) return hipErrorInvalidValue;
-  k_wgrad<1><<<grid, 256, 0, s>>>(job, job, expert_offsets, max_rows, E);
+  k_wgrad<1, false><<<grid, 256, 0, s>>>(job, job, expert_offsets, max_rows, E, 1);
   return hipGetLastError();
+}
+
+// Ranges of rows, as many as the places for tiles take, where the stages they take
+// off a tile (0.55 us each, for an expert's even share) cost more than the float32
+// sums, written and read at the rate of a copy, and their launch.  The backward
+// with its checkpoint: 20000 rows, 1 expert, 256 x 256: 420 us whole, 93 in 16
+// ranges; 65536 rows, 1 expert, 128 x 128: 1244 and 142; 1905 rows, 1 expert,
+// 64 x 1344: 82 and 60; 546 rows, 2 experts, 192 x 2624 (whole by this rule): 74
+// and, in two ranges, 84.
+int ffn_wgrad_split(int64_t max_rows, int E, int d, int I) {
+  const int64_t tiles = E * (ceil_div(I, kBM) * ceil_div(d, kBN) + ceil_div(d, kBM) * ceil_div(2 * I, kBN));
+  const int64_t room = 2 * (int64_t)device_cus() / tiles;
+  const double stages = (double)max_rows / ((double)E * kBK);
+  const double sum_us = 2.0 * 4 * 3 * (double)E * d * I / 4.8e6;
+  int best = 1;
+  double best_us = 0.9 * 0.55 * stages;
+  for (int sp = 2; sp <= kWgradSplitMax && sp <= room; ++sp) {
+    const double us = 0.55 * stages / sp + sp * sum_us + 5;
+    if (us < best_us) {
+      best = sp;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 hipError_t launch_ffn_wgrad_bf16(const bf16_t* x, const bf16_t* dy, const bf16_t* h, const bf16_t* dgu,
                                  const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
-                                 bf16_t* dw_gate_up, bf16_t* dw_down, hipStream_t s) {
-  const Job down = make_job(h, I, I, dy, d, d, dw_down), gate_up = make_job(x, d, d, dgu, 2 * I, 2 * I, dw_gate_up);
-  const unsigned grid =
-      grid_of((int64_t)E * ((int64_t)down.m_tiles * down.n_tiles + (int64_t)gate_up.m_tiles * gate_up.n_tiles));
+                                 bf16_t* dw_gate_up, bf16_t* dw_down, int n_split, float* part, hipStream_t s) {
+  Job down = make_job(h, I, I, dy, d, d, dw_down), gate_up = make_job(x, d, d, dgu, 2 * I, 2 * I, dw_gate_up);
+  const unsigned grid = grid_of(
+      n_split * ((int64_t)E * ((int64_t)down.m_tiles * down.n_tiles + (int64_t)gate_up.m_tiles * gate_up.n_tiles)));
   if (grid == 0) return hipErrorInvalidValue;
-  k_wgrad<2><<<grid, 256, 0, s>>>(down, gate_up, expert_offsets, max_rows, E);
+  if (n_split == 1) {
+    k_wgrad<2, false><<<grid, 256, 0, s>>>(down, gate_up, expert_offsets, max_rows, E, 1);
+    return hipGetLastError();
+  }
+  down.part = part;
+  gate_up.part = part + (int64_t)n_split * E * I * d;
+  k_wgrad<2, true><<<grid, 256, 0, s>>>(down, gate_up, expert_offsets, max_rows, E, n_split);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t blocks = ceil_div((int64_t)E * 3 * d * I, 1024);
+  k_wgrad_sum<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(down, gate_up, E, n_split);
   return hipGetLastError();
 }
 
