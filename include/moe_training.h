@@ -12,6 +12,9 @@
  * multiples of their own 4.  Limits beside moe.h's: d and I below 2^21, grouped
  * rows * max(d, 2I) below 2^31, E * 2*d*I below 2^34.
  *
+ * A workspace size holds for its arguments alone: fewer rows can need a larger
+ * one (the products of few rows are cut into ranges, summed from there).
+ *
  * The 8-bit checkpoint.  What the backward needs of the forward, beside x and
  * the weights, are the pre-activations g | u = x Wgu of every grouped row;
  * h = silu(g) u is formed from them again and y is not needed.  They are kept
@@ -40,7 +43,8 @@ extern "C" {
  * moe_grouped_ffn for a training step, for rows that were grouped elsewhere
  * (the rows an expert-parallel rank received).
  *
- * moe_grouped_ffn_train: y_perm exactly as moe_grouped_ffn computes it, and
+ * moe_grouped_ffn_train: y_perm by moe_grouped_ffn's formula and roundings (g
+ * and u unrounded into h, h to bf16, y once; the order of sums may differ), and
  * the 8-bit checkpoint of the rows' g | u.
  *
  * moe_grouped_ffn_backward: gradients of <dy_perm, y_perm>.  For row r of
@@ -49,9 +53,10 @@ extern "C" {
  *   dx = [dg | du] Wgu[e]^T;  dW_gate_up[e] = sum_r x^T [dg | du]
  *   dW_down[e] = sum_r h^T dy           (zero for an expert without rows)
  * gu_q and gu_s: a checkpoint, or both NULL: g | u are computed again from x
- * (not rounded to 8 bits).  bf16: float32 accumulation;
- * h, dg and du are rounded to bf16 before the products that read them, and
- * every gradient once; MOE_F32: float32 throughout.  The order of every sum
+ * (MOE_BF16: held meanwhile as whole multiples of a scale as above, of 16 bits,
+ * off by at most amax / 65534).  MOE_BF16: float32 accumulation; h, dg and du
+ * are rounded to bf16 before the products that read them, and every gradient
+ * once; MOE_F32: float32 throughout.  The order of every sum
  * depends on the sizes only, so equal calls give equal bits.
  *   x_perm, dy_perm [max_rows, d] dt; expert_offsets [E+1]
  *   y_perm, dx_perm [max_rows, d] dt (outputs; rows >= expert_offsets[E], of
@@ -72,14 +77,18 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
                                     void* stream);
 
 /* ---- the whole layer with an 8-bit checkpoint ------------------------------------
- * moe_forward_train_q8: out, topk_idx and topk_w exactly as moe_forward
- * computes them (logits, or given pairs), the grouping and the checkpoint.
+ * moe_forward_train_q8: topk_idx and topk_w exactly as moe_forward computes
+ * them (from logits, or given pairs), out by its formula, the grouping and the
+ * checkpoint.  MOE_BF16 rounds h and then out: the experts' rows y stay float32
+ * up to out's one rounding, where moe_forward rounds them too.
  * The caller keeps expert_offsets [E+1], row_token [T*k], pair_row [T*k],
  * gu_q [T*k, 2I] and gu_s [T*k, 2, I/64] for the backward; the workspace is
  * free again when the call's work has run.
  *
  * moe_backward_q8: gradients of <dout, out>, as moe_backward defines them, at
- * the checkpoint's g and u.  With y not kept, a routing weight's gradient is
+ * the checkpoint's g and u.  The routing weight goes into h and [dg | du] before
+ * they are rounded, so that every product reads dout as it is, and a token's dx
+ * is summed from float32 rows and rounded once.  With y not kept, a routing weight's gradient is
  * taken on the other side of the down projection:
  *   dtopk_w[p] = <dout_t, h_p Wd[e]> = <dout_t Wd[e]^T, h_p>
  *   dlogits[t, e_j] = w_j (dtopk_w_j - sum_i w_i dtopk_w_i) for the weights of

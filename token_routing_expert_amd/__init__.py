@@ -530,7 +530,7 @@ def moe_backward(x, w_gate_up, w_down, k: int, dout, logits=None, topk_idx=None,
 
 # ---- serving entry points (include/moe_serving.h) -----------------------------------
 #
-# (These and the training entry points.)  Tensors of one call live on one GPU, which need not be the current one; what
+# Tensors of one call, here and of the training entry points, live on one GPU, which need not be the current one; what
 # a call allocates itself belongs to the stream it runs on.
 
 FEW_MAX_TOKENS = 64
@@ -846,8 +846,8 @@ def moe_grouped_ffn_train_workspace_size(max_rows: int, E: int, d: int, I: int, 
 def moe_grouped_ffn_train(x_perm, expert_offsets, w_gate_up, w_down, y_perm=None, gu_q=None, gu_s=None,
                           workspace=None, stream=None):
     """moe_grouped_ffn for a training step: x_perm [R, d] rows grouped by expert_offsets [E+1] ->
-    (y_perm [R, d], gu_q [R, 2I] int8, gu_s [R, 2, I/64] float32); y_perm as moe_grouped_ffn computes it, and the
-    8-bit checkpoint of the rows' pre-activations for moe_grouped_ffn_backward."""
+    (y_perm [R, d], gu_q [R, 2I] int8, gu_s [R, 2, I/64] float32); y_perm by moe_grouped_ffn's
+    formula, and the 8-bit checkpoint of the rows' pre-activations for moe_grouped_ffn_backward."""
     torch = _torch()
     lib = load()
     R, d = x_perm.shape
@@ -908,8 +908,8 @@ def moe_forward_train_q8_workspace_size(T: int, d: int, E: int, k: int, I: int, 
 
 def moe_forward_train_q8(x, w_gate_up, w_down, k: int, logits=None, topk_idx=None, topk_w=None, out=None, kept=None,
                          workspace=None, stream=None):
-    """The forward of a training step: ``out`` as moe_forward computes it, and what the backward needs in a
-    Checkpoint (``kept``: one to fill again, new tensors when None).  The workspace is free again when the call's
+    """The forward of a training step: ``out`` by moe_forward's formula (bf16: the experts' rows stay float32 up to
+    out's one rounding), the routing exactly as moe_forward computes it, and what the backward needs in a Checkpoint (``kept``: one to fill again, new tensors when None).  The workspace is free again when the call's
     work has run.  Returns (out [T, d], topk_idx, topk_w, Checkpoint)."""
     torch = _torch()
     lib = load()
