@@ -56,11 +56,27 @@ bool sizes_positive(int64_t rows, int32_t d, int32_t E, int32_t I, moe_dtype dt)
 struct FfnLayout {
   size_t h, gu, extra, y, split, sched, total;
   int gu_split, y_split;
+  bool few;
 };
 
+// Of few tiles, whether gate/up is the bf16 product with its k-stages in ranges: a
+// tile in float32 walks all of d by itself (the forward of 16 rows, 1 expert, 2560 x
+// 64: 60 us, in ranges 21; 4 rows, 3 experts, 1536 x 128: 40 and 19).
+bool few_wide(int64_t d, moe_dtype dt) { return dt == MOE_BF16 && d > 768; }
+
 FfnLayout ffn_layout(int64_t rows, int64_t d, int64_t E, int64_t I, moe_dtype dt, bool rows32) {
-  FfnLayout L;
+  FfnLayout L{};
   size_t o = 0;
+  L.few = small_products(rows, (int)E, (int)d, (int)I, dt == MOE_BF16);
+  if (L.few) {   // h, g | u of a wide product, and (a layer's) y
+    L.h = o; o += align256((size_t)(rows * I) * 4);
+    L.gu_split = few_wide(d, dt) ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 0;
+    L.gu = o; o += align256((size_t)(L.gu_split * rows * 2 * I) * 4);
+    L.y = o; o += rows32 ? align256((size_t)(rows * d) * 4) : 0;
+    L.y_split = 1;
+    L.total = o;
+    return L;
+  }
   L.gu_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 1;
   L.y_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)I, (int)d) : 0;
   if (!rows32 && L.y_split == 1) L.y_split = 0;
@@ -83,9 +99,11 @@ LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, 
   LayerLayout L;
   size_t o = 0;
   L.perm_ws = o; o += permute_index_workspace(P, (int)E);
-  L.x_perm = o;  o += dt == MOE_F32 ? align256((size_t)(P * d) * 4) : 0;   // bf16 gathers rows in place
-  L.y = o;       o += dt == MOE_F32 ? align256((size_t)(P * d) * 4) : 0;   // bf16: among the products'
-  L.ffn = o;     o += ffn_layout(P, d, E, I, dt, true).total;
+  const FfnLayout F = ffn_layout(P, d, E, I, dt, true);
+  const size_t f32 = dt == MOE_F32 && !F.few ? align256((size_t)(P * d) * 4) : 0;
+  L.x_perm = o;  o += f32;   // (the others gather rows in place, and have y among the products')
+  L.y = o;       o += f32;
+  L.ffn = o;     o += F.total;
   L.total = o;
   return L;
 }
@@ -99,12 +117,27 @@ LayerLayout layer_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, 
 struct GradLayout {
   size_t h, dgu, gu, gu_s, extra, gu32, dh, dx, dw, total;
   int gu_split, dh_split, dx_split, dw_split;   // ranges of the row gradients' k and of the weight gradients' rows
+  bool few;                                     // the kernels of few tiles
 };
 
 GradLayout grad_layout(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt, bool layer) {
   const size_t s = elem_size(dt);
   const bool again = !layer;
-  GradLayout L;
+  GradLayout L{};
+  L.few = small_products(rows, (int)E, (int)d, (int)I, dt == MOE_BF16);
+  if (L.few) {
+    size_t o = 0;
+    L.h = o;   o += align256((size_t)(rows * I) * 4);
+    L.dgu = o; o += align256((size_t)(rows * 2 * I) * 4);
+    L.gu_split = again && few_wide(d, dt) ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 0;
+    L.gu32 = o; o += align256((size_t)(L.gu_split * rows * 2 * I) * 4);
+    L.gu = o;   o += L.gu_split ? align256((size_t)(rows * 2 * I) * 2) : 0;
+    L.gu_s = o; o += L.gu_split ? align256((size_t)(rows * 2 * (I / kKeepBlock)) * 4) : 0;
+    L.dx = o;  o += layer ? align256((size_t)(rows * d) * 4) : 0;
+    L.dx_split = 1;
+    L.total = o;
+    return L;
+  }
   L.gu_split = dt == MOE_BF16 && again ? rows_split(rows, (int)E, (int)d, (int)(2 * I)) : 1;
   L.dh_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)d, (int)I) : 1;
   L.dx_split = dt == MOE_BF16 ? rows_split(rows, (int)E, (int)(2 * I), (int)d) : layer ? 1 : 0;
@@ -133,8 +166,8 @@ struct BackwardLayout {
 };
 
 int64_t dot_columns(int64_t rows, int64_t E, int64_t d, int64_t I, moe_dtype dt) {
-  if (dt == MOE_BF16) return rows_split(rows, (int)E, (int)d, (int)I) > 1 ? 1 : dot_parts((int)I);
-  return small_f32(rows, (int)E, (int)d, (int)I) ? I / 32 : 1;
+  if (small_products(rows, (int)E, (int)d, (int)I, dt == MOE_BF16)) return I / 32;
+  return dt == MOE_F32 || rows_split(rows, (int)E, (int)d, (int)I) > 1 ? 1 : dot_parts((int)I);
 }
 
 BackwardLayout backward_layout(int64_t T, int64_t d, int64_t E, int64_t k, int64_t I, moe_dtype dt) {
@@ -166,10 +199,26 @@ moe_status gate_up_keep(const bf16_t* x, int64_t x_rows, const int32_t* row_toke
                         int gu_split, float* gu, hipStream_t s, int32_t* sched) {
   if (gu_split > 1) {
     TRY(from_hip(launch_gate_up_rows32(x, offs, rows, E, d, I, wgu, gu, gu_split, s, row_token, x_rows)));
-    return from_hip(launch_keep_rows(gu, gu_split, offs, E, rows, I, kept, bits, h, s));
+    return from_hip(launch_keep_rows(gu, gu_split, offs, E, rows, I, kept, bits, h, nullptr, s));
   }
   if (bits == 16) return from_hip(launch_gate_up_keep16_bf16(x, offs, rows, E, d, I, wgu, kept, s, sched));
   return from_hip(launch_gate_up_keep8_bf16(x, offs, rows, E, d, I, wgu, h, kept, s, row_token, x_rows, sched));
+}
+
+// The forward of few tiles (gu_split: ranges of gate/up's bf16 product; 0: in float32).
+template <typename T, typename O>
+moe_status few_rows(const T* x, int64_t x_rows, const int32_t* row_token, const int32_t* offs, int64_t rows, int32_t E,
+                    int32_t d, int32_t I, const T* wgu, const T* wd, float* h, const Kept& kept, int gu_split,
+                    float* gu, O* y, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (gu_split) {
+      TRY(from_hip(launch_gate_up_rows32(x, offs, rows, E, d, I, wgu, gu, gu_split, s, row_token, x_rows)));
+      TRY(from_hip(launch_keep_rows(gu, gu_split, offs, E, rows, I, kept, 8, nullptr, h, s)));
+      return from_hip(launch_small_down(h, offs, rows, E, d, I, wd, y, s));
+    }
+  }
+  TRY(from_hip(launch_small_gate_up(x, x_rows, row_token, offs, rows, E, d, I, wgu, h, kept, s)));
+  return from_hip(launch_small_down(h, offs, rows, E, d, I, wd, y, s));
 }
 
 // w [dg | du], w h and the parts of <dh, h> of rows with gradient dy, the same way.
@@ -191,9 +240,9 @@ moe_status grad_rows_f32(const float* x, const float* dy, const float* row_w, co
                          hipStream_t s) {
   const bool again = kept.q == nullptr;
   float *h = (float*)(ws + L.h), *dgu = (float*)(ws + L.dgu), *gu = (float*)(ws + L.gu), *dh = (float*)(ws + L.dh);
-  if (small_f32(rows, E, d, I))
-    return from_hip(launch_small_grads_f32(x, dy, offs, rows, E, d, I, wgu, wd, kept, row_w, dgu, h, dot, dx,
-                                           dw_gate_up, dw_down, s));
+  if (L.few)
+    return from_hip(launch_small_grads(x, dy, offs, rows, E, d, I, wgu, wd, kept, 8, row_w, dgu, h, dot, dx,
+                                       dw_gate_up, dw_down, s));
   if (again) TRY(from_hip(launch_gate_up_save_f32(x, offs, rows, E, d, I, wgu, h, gu, s)));
   TRY(from_hip(launch_down_dgrad_f32(dy, offs, rows, E, d, I, wd, dh, s)));
   TRY(from_hip(launch_swiglu_bwd_f32(dh, again ? gu : nullptr, kept, row_w, offs, E, rows, I, dgu, h, dot, s)));
@@ -224,14 +273,16 @@ moe_status moe_grouped_ffn_train(const void* x_perm, const int32_t* expert_offse
   char* ws = (char*)workspace;
   const Kept kept{(int8_t*)gu_q, gu_s, (float*)(ws + L.extra)};
   hipStream_t s = (hipStream_t)stream;
+  if (L.few) {
+    float *h = (float*)(ws + L.h), *gu = (float*)(ws + L.gu);
+    if (dt == MOE_F32)
+      return few_rows((const float*)x_perm, 0, nullptr, expert_offsets, max_rows, E, d, I, (const float*)w_gate_up,
+                      (const float*)w_down, h, kept, 0, gu, (float*)y_perm, s);
+    return few_rows((const bf16_t*)x_perm, 0, nullptr, expert_offsets, max_rows, E, d, I, (const bf16_t*)w_gate_up,
+                    (const bf16_t*)w_down, h, kept, L.gu_split, gu, (bf16_t*)y_perm, s);
+  }
   if (dt == MOE_F32) {
     float *h = (float*)(ws + L.h), *gu = (float*)(ws + L.gu);
-    if (small_f32(max_rows, E, d, I)) {
-      TRY(from_hip(launch_small_gate_up_f32((const float*)x_perm, 0, nullptr, expert_offsets, max_rows, E, d, I,
-                                            (const float*)w_gate_up, h, kept, s)));
-      return from_hip(launch_small_down_f32(h, expert_offsets, max_rows, E, d, I, (const float*)w_down,
-                                            (float*)y_perm, s));
-    }
     TRY(from_hip(launch_gate_up_save_f32((const float*)x_perm, expert_offsets, max_rows, E, d, I,
                                          (const float*)w_gate_up, h, gu, s)));
     TRY(from_hip(launch_keep8_f32(gu, expert_offsets, E, max_rows, I, kept, s)));
@@ -279,8 +330,19 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
                          (float*)dw_down, nullptr, ws, L, s);
   const bf16_t *x = (const bf16_t*)x_perm, *dy = (const bf16_t*)dy_perm, *wgu = (const bf16_t*)w_gate_up,
                *wd = (const bf16_t*)w_down;
-  bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
   const Kept again{(int8_t*)(ws + L.gu), (float*)(ws + L.gu_s), (float*)(ws + L.extra)};
+  if (L.few) {
+    const bool wide = !gu_q && L.gu_split;
+    if (wide) {
+      float* gu = (float*)(ws + L.gu32);
+      TRY(from_hip(launch_gate_up_rows32(x, expert_offsets, max_rows, E, d, I, wgu, gu, L.gu_split, s, nullptr, 0)));
+      TRY(from_hip(launch_keep_rows(gu, L.gu_split, expert_offsets, E, max_rows, I, again, 16, nullptr, nullptr, s)));
+    }
+    return from_hip(launch_small_grads(x, dy, expert_offsets, max_rows, E, d, I, wgu, wd, wide ? again : kept,
+                                       wide ? 16 : 8, nullptr, (float*)(ws + L.dgu), (float*)(ws + L.h), nullptr,
+                                       (bf16_t*)dx_perm, (bf16_t*)dw_gate_up, (bf16_t*)dw_down, s));
+  }
+  bf16_t *h = (bf16_t*)(ws + L.h), *dgu = (bf16_t*)(ws + L.dgu);
   if (!gu_q)
     TRY(gate_up_keep(x, 0, nullptr, expert_offsets, max_rows, E, d, I, wgu, nullptr, again, 16, L.gu_split,
                      (float*)(ws + L.gu32), s, nullptr));
@@ -322,15 +384,20 @@ moe_status moe_forward_train_q8(const void* x, const float* logits, int32_t T, i
   const Kept kept{(int8_t*)gu_q, gu_s, (float*)(fws + F.extra)};
   hipStream_t s = (hipStream_t)stream;
   if (logits) TRY(from_hip(launch_route_topk(logits, T, E, k, topk_idx, topk_w, s)));
-  if (dt == MOE_F32) {
-    float *xp = (float*)(ws + L.x_perm), *h = (float*)(fws + F.h), *gu = (float*)(fws + F.gu), *y = (float*)(ws + L.y);
-    if (small_f32(P, E, d, I)) {
-      TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s)));
-      TRY(from_hip(launch_small_gate_up_f32((const float*)x, T, row_token, expert_offsets, P, E, d, I,
-                                            (const float*)w_gate_up, h, kept, s)));
-      TRY(from_hip(launch_small_down_f32(h, expert_offsets, P, E, d, I, (const float*)w_down, y, s)));
+  if (F.few) {
+    float *h = (float*)(fws + F.h), *gu = (float*)(fws + F.gu), *y = (float*)(fws + F.y);
+    TRY(from_hip(launch_permute_index(topk_idx, P, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s)));
+    if (dt == MOE_F32) {
+      TRY(few_rows((const float*)x, T, row_token, expert_offsets, P, E, d, I, (const float*)w_gate_up,
+                   (const float*)w_down, h, kept, 0, gu, y, s));
       return from_hip(launch_combine_f32(y, P, pair_row, topk_w, T, k, d, (float*)out, s));
     }
+    TRY(few_rows((const bf16_t*)x, T, row_token, expert_offsets, P, E, d, I, (const bf16_t*)w_gate_up,
+                 (const bf16_t*)w_down, h, kept, F.gu_split, gu, y, s));
+    return from_hip(launch_combine_rows32(y, 1, P, pair_row, topk_w, T, k, d, (bf16_t*)out, s));
+  }
+  if (dt == MOE_F32) {
+    float *xp = (float*)(ws + L.x_perm), *h = (float*)(fws + F.h), *gu = (float*)(fws + F.gu), *y = (float*)(ws + L.y);
     TRY(from_hip(launch_permute_rows(topk_idx, T, k, E, row_token, pair_row, expert_offsets, ws + L.perm_ws, s,
                                      nullptr, x, (int64_t)d * 4, xp)));
     TRY(from_hip(launch_gate_up_save_f32(xp, expert_offsets, P, E, d, I, (const float*)w_gate_up, h, gu, s)));
@@ -387,18 +454,25 @@ moe_status moe_backward_q8(const void* x, int32_t T, int32_t d, int32_t E, int32
     TRY(grad_rows_f32((const float*)x_perm, (const float*)dout_perm, row_w, expert_offsets, P, E, d, I,
                       (const float*)w_gate_up, (const float*)w_down, kept, dxp, (float*)dw_gate_up, (float*)dw_down,
                       dot, gws, G, s));
-    return from_hip(launch_combine_grad_f32(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
-                                            (float*)dx, dtopk_w, dlogits, s));
+    return from_hip(launch_combine_grad_f32(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w,
+                                            topk_idx, T, k, d, E, (float*)dx, dtopk_w, dlogits, s));
   }
   const bf16_t *xp = (const bf16_t*)x_perm, *dyp = (const bf16_t*)dout_perm, *wgu = (const bf16_t*)w_gate_up,
                *wd = (const bf16_t*)w_down;
-  bf16_t *h = (bf16_t*)(gws + G.h), *dgu = (bf16_t*)(gws + G.dgu);
-  TRY(down_bwd(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, G.dh_split, (float*)(gws + G.dh), s));
-  TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, G.dx_split, s)));
-  TRY(from_hip(launch_ffn_wgrad_bf16(xp, dyp, h, dgu, expert_offsets, P, E, d, I, (bf16_t*)dw_gate_up,
-                                     (bf16_t*)dw_down, G.dw_split, (float*)(gws + G.dw), s)));
-  return from_hip(launch_combine_grad_bf16(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w, topk_idx, T, k, d, E,
-                                           (bf16_t*)dx, dtopk_w, dlogits, s));
+  if (G.few) {
+    TRY(from_hip(launch_small_grads(xp, dyp, expert_offsets, P, E, d, I, wgu, wd, kept, 8, row_w,
+                                    (float*)(gws + G.dgu), (float*)(gws + G.h), dot, dxp, (bf16_t*)dw_gate_up,
+                                    (bf16_t*)dw_down, s)));
+  } else {
+    bf16_t *h = (bf16_t*)(gws + G.h), *dgu = (bf16_t*)(gws + G.dgu);
+    TRY(down_bwd(dyp, expert_offsets, P, E, d, I, wd, kept, 8, row_w, dgu, h, dot, G.dh_split, (float*)(gws + G.dh),
+                 s));
+    TRY(from_hip(launch_gate_up_dgrad_rows32(dgu, expert_offsets, P, E, d, I, wgu, dxp, G.dx_split, s)));
+    TRY(from_hip(launch_ffn_wgrad_bf16(xp, dyp, h, dgu, expert_offsets, P, E, d, I, (bf16_t*)dw_gate_up,
+                                       (bf16_t*)dw_down, G.dw_split, (float*)(gws + G.dw), s)));
+  }
+  return from_hip(launch_combine_grad_bf16(dxp, G.dx_split, dot, dot_columns(P, E, d, I, dt), P, pair_row, topk_w,
+                                           topk_idx, T, k, d, E, (bf16_t*)dx, dtopk_w, dlogits, s));
 }
 
 moe_status moe_checkpoint_values(const void* gu_q, const float* gu_s, int32_t rows, int32_t I, moe_dtype dt, void* gu,

@@ -375,9 +375,9 @@ hipError_t launch_gate_up_rows32(const bf16_t* x, const int32_t* expert_offsets,
                                  const int32_t* row_token, int64_t x_rows);
 hipError_t launch_down_dgrad_rows32(const bf16_t* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
                                     int I, const bf16_t* w_down, float* dh, int n_split, hipStream_t s);
-// the checkpoint (bits: 8 or 16) and, of 8 bits, h of gu's rows
+// the checkpoint (bits: 8 or 16) and, of 8 bits, h of gu's rows (one of h and h32)
 hipError_t launch_keep_rows(const float* gu, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
-                            const Kept& kept, int bits, bf16_t* h, hipStream_t s);
+                            const Kept& kept, int bits, bf16_t* h, float* h32, hipStream_t s);
 // dgu, h and dot [max_rows] as launch_down_bwd_bf16's
 hipError_t launch_swiglu_bwd_rows(const float* dh, int n_split, const Kept& kept, int bits, const float* row_w,
                                   const int32_t* expert_offsets, int E, int64_t max_rows, int I, bf16_t* dgu,
@@ -405,22 +405,25 @@ hipError_t launch_combine_grad_f32(const float* dx_perm, int n_split, const floa
                                    const int32_t* pair_row, const float* pair_w, const int32_t* topk_idx, int64_t T,
                                    int k, int d, int E, float* dx, float* dw, float* dlogits, hipStream_t s);
 
-// ---- float32 products of few tiles (small_f32.hip) ----
-// whether a training call's float32 products take them
-bool small_f32(int64_t max_rows, int E, int d, int I);
-// h and the checkpoint; with row_token, row r's x is row row_token[r] of x [x_rows, d]
-hipError_t launch_small_gate_up_f32(const float* x, int64_t x_rows, const int32_t* row_token,
-                                    const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
-                                    const float* w_gate_up, float* h, const Kept& kept, hipStream_t s);
-hipError_t launch_small_down_f32(const float* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
-                                 const float* w_down, float* y, hipStream_t s);
-// every gradient of grouped rows, from the checkpoint or, where kept.q is null,
+// ---- products of few tiles in float32, of operands T = float or bf16 (small_f32.hip) ----
+// whether a call's tiles are that few
+bool small_products(int64_t max_rows, int E, int d, int I, bool bf16);
+// with row_token, row r's x is row row_token[r] of x (x_rows of them)
+template <typename T>
+hipError_t launch_small_gate_up(const T* x, int64_t x_rows, const int32_t* row_token, const int32_t* expert_offsets,
+                                int64_t max_rows, int E, int d, int I, const T* w_gate_up, float* h, const Kept& kept,
+                                hipStream_t s);
+template <typename T, typename O>
+hipError_t launch_small_down(const float* h, const int32_t* expert_offsets, int64_t max_rows, int E, int d, int I,
+                             const T* w_down, O* y, hipStream_t s);
+// every gradient of grouped rows, from the checkpoint (of 8 or 16 bits) or, where kept.q is null,
 // from g | u computed again; dgu [max_rows, 2I] and h [max_rows, I] are scratch;
 // row_w and dot ([max_rows, I / 32] parts) as launch_down_bwd_bf16's
-hipError_t launch_small_grads_f32(const float* x, const float* dy, const int32_t* expert_offsets, int64_t max_rows,
-                                  int E, int d, int I, const float* w_gate_up, const float* w_down, const Kept& kept,
-                                  const float* row_w, float* dgu, float* h, float* dot, float* dx, float* dw_gate_up,
-                                  float* dw_down, hipStream_t s);
+template <typename T, typename O>
+hipError_t launch_small_grads(const T* x, const T* dy, const int32_t* expert_offsets, int64_t max_rows, int E, int d,
+                              int I, const T* w_gate_up, const T* w_down, const Kept& kept, int bits,
+                              const float* row_w, float* dgu, float* h, float* dot, O* dx, T* dw_gate_up, T* dw_down,
+                              hipStream_t s);
 
 // ---- 8-bit codes and scales (quantize.hip) ----
 // rows and expert weights to e4m3 with a float32 scale for each block of 128

@@ -75,10 +75,10 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 }
 
 // One block of a row's checkpoint by 16 lanes, four columns each (v[0] its gates,
-// v[1] its ups, at column c of I): codes and scales, and of 8 bits h in bf16.
-template <int BITS>
+// v[1] its ups, at column c of I): codes and scales, and of 8 bits h in bf16 or float32.
+template <int BITS, typename H>
 __device__ __forceinline__ void keep_block(const f32x4 (&v)[2], int64_t row, int c, int I, int l16, const Kept& kept,
-                                           bf16_t* __restrict__ h) {
+                                           H* __restrict__ h) {
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     uint32_t m = 0;
@@ -97,7 +97,10 @@ __device__ __forceinline__ void keep_block(const f32x4 (&v)[2], int64_t row, int
     float f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = v[0][i] * __builtin_amdgcn_rcpf(1.f + __expf(-v[0][i])) * v[1][i];
-    *(uint2*)(h + row * I + c) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    if constexpr (sizeof(H) == 4)
+      *(f32x4*)(h + row * I + c) = f32x4{f[0], f[1], f[2], f[3]};
+    else
+      *(uint2*)(h + row * I + c) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
   }
 }
 

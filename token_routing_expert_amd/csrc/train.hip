@@ -102,10 +102,10 @@ __device__ __forceinline__ f32x4 add_ranges(const float* __restrict__ p, int n_s
 }
 
 // 16 lanes take a row's block of 64 gates and ups.
-template <int BITS>
+template <int BITS, typename H>
 __global__ __launch_bounds__(kThreads) void k_keep_rows(const float* __restrict__ gu, int n_split,
                                                         const int32_t* __restrict__ offsets, int E, int64_t max_rows,
-                                                        int I, Kept kept, bf16_t* __restrict__ h) {
+                                                        int I, Kept kept, H* __restrict__ h) {
   const int nb = I / kKeepBlock;
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 16;
   const int64_t row = item / nb;
@@ -244,9 +244,13 @@ hipError_t launch_swiglu_bwd_f32(const float* dh, const float* gu, const Kept& k
 }
 
 hipError_t launch_keep_rows(const float* gu, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows, int I,
-                            const Kept& kept, int bits, bf16_t* h, hipStream_t s) {
+                            const Kept& kept, int bits, bf16_t* h, float* h32, hipStream_t s) {
   const unsigned blocks = blocks_of(max_rows * (I / kKeepBlock), kThreads / 16);
-  const auto kernel = bits == 16 ? k_keep_rows<16> : k_keep_rows<8>;
+  if (h32) {
+    k_keep_rows<8><<<blocks, kThreads, 0, s>>>(gu, n_split, expert_offsets, E, max_rows, I, kept, h32);
+    return hipGetLastError();
+  }
+  const auto kernel = bits == 16 ? k_keep_rows<16, bf16_t> : k_keep_rows<8, bf16_t>;
   kernel<<<blocks, kThreads, 0, s>>>(gu, n_split, expert_offsets, E, max_rows, I, kept, h);
   return hipGetLastError();
 }
