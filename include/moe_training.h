@@ -44,7 +44,8 @@ extern "C" {
  * (the rows an expert-parallel rank received).
  *
  * moe_grouped_ffn_train: y_perm by moe_grouped_ffn's formula and roundings (g
- * and u unrounded into h, h to bf16, y once; the order of sums may differ), and
+ * and u unrounded into h, h to bf16, y once; the order of sums may differ, and
+ * h stays float32 where it does in the backward), and
  * the 8-bit checkpoint of the rows' g | u.
  *
  * moe_grouped_ffn_backward: gradients of <dy_perm, y_perm>.  For row r of
@@ -55,8 +56,9 @@ extern "C" {
  * gu_q and gu_s: a checkpoint, or both NULL: g | u are computed again from x
  * (MOE_BF16: held meanwhile as whole multiples of a scale as above, of 16 bits,
  * off by at most amax / 65534).  MOE_BF16: float32 accumulation; h, dg and du
- * are rounded to bf16 before the products that read them, and every gradient
- * once; MOE_F32: float32 throughout.  The order of every sum
+ * are rounded to bf16 before the products that read them (in calls of few rows
+ * and narrow experts they stay float32, by a rule on the sizes), and every
+ * gradient once; MOE_F32: float32 throughout.  The order of every sum
  * depends on the sizes only, so equal calls give equal bits.
  *   x_perm, dy_perm [max_rows, d] dt; expert_offsets [E+1]
  *   y_perm, dx_perm [max_rows, d] dt (outputs; rows >= expert_offsets[E], of
@@ -79,8 +81,9 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
 /* ---- the whole layer with an 8-bit checkpoint ------------------------------------
  * moe_forward_train_q8: topk_idx and topk_w exactly as moe_forward computes
  * them (from logits, or given pairs), out by its formula, the grouping and the
- * checkpoint.  MOE_BF16 rounds h and then out: the experts' rows y stay float32
- * up to out's one rounding, where moe_forward rounds them too.
+ * checkpoint.  MOE_BF16 rounds h (where the backward does) and then out: the
+ * experts' rows y stay float32 up to out's one rounding, where moe_forward
+ * rounds them too.
  * The caller keeps expert_offsets [E+1], row_token [T*k], pair_row [T*k],
  * gu_q [T*k, 2I] and gu_s [T*k, 2, I/64] for the backward; the workspace is
  * free again when the call's work has run.

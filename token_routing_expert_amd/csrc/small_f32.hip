@@ -14,7 +14,8 @@
 // What such a call costs is its launches and one memory round trip each, so the
 // steps are few: the SwiGLU backward sits behind dh (with g | u computed again
 // beside it where there is no checkpoint), and dx and both weight gradients, which
-// do not read one another, are one launch.  Measured: at small_f32 below.
+// do not read one another, are one launch.  Measured: at
+// small_products below.
 #include "keep8.hpp"
 
 #include <algorithm>
