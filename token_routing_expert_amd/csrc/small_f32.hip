@@ -410,8 +410,9 @@ bool small_products(int64_t max_rows, int E, int d, int I, bool bf16) {
   const int64_t tiles = max_rows / 64 + std::min<int64_t>(E, max_rows);
   const int width = std::min(d, I);
   const int64_t t = tiles * ceil_div(width, 128);
-  if (bf16)
-    return max_rows * width <= 8192 || (max_rows <= 400 * (int64_t)E && t <= 64 && std::max(d, I) <= 768);
+  if (bf16)   // (2^32: the weight gradients' tiles have to fit a grid of 2^32 threads)
+    return (max_rows * width <= 8192 && (int64_t)E * d * I <= ((int64_t)1 << 32)) ||
+           (max_rows <= 400 * (int64_t)E && t <= 64 && std::max(d, I) <= 768);
   return ((max_rows <= 128 * (int64_t)E && t <= 160) || (max_rows <= 1024 * (int64_t)E && t <= 80)) &&
          (int64_t)E * d * I <= ((int64_t)1 << 24);
 }
