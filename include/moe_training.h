@@ -10,7 +10,7 @@
  * Rows, weights, gradients, codes and workspaces begin at multiples of 16
  * bytes (MOE_ERR_ARG otherwise); scales, indices and routing weights at
  * multiples of their own 4.  Limits beside moe.h's: d and I below 2^21, grouped
- * rows * max(d, 2I) below 2^31, E * 2*d*I below 2^34.
+ * rows * max(d, 2I) below 2^31, E * 2*d*I below 2^34, a layer's T*d below 2^30.
  *
  * A workspace size holds for its arguments alone: fewer rows can need a larger
  * one (the products of few rows are cut into ranges, summed from there).
