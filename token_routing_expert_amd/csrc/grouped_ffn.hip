@@ -191,28 +191,30 @@ struct Tile {
 };
 
 // The rows of one tile in a row-major array of row_bytes a row, behind a buffer
-// descriptor: a lane's offset is 32 bits, what is the same for a wave goes into
-// a scalar, and rows past the tile's are not stored and read as zeros.
+// descriptor: a lane's offset is 32 bits, rows past the tile's are not stored and
+// read as zeros.  What is the same for a wave (scalar) is added to the lane's
+// offset here and not left to the instruction, for two reasons.  A scalar offset
+// lies outside the bounds check (as the compiler documents it), so rows past the
+// tile's could be read, behind an array's last row too.  And behind a
+// 16-byte store without a scalar offset the compiler keeps its data registers for
+// one more instruction; with one it does not, and the next instruction's result
+// was seen in the stored rows on gfx950.
 struct TileRows {
   __amdgpu_buffer_rsrc_t rsrc;
   __device__ __forceinline__ TileRows(const void* base, int64_t row0, int rows, int row_bytes)
       : rsrc(__builtin_amdgcn_make_buffer_rsrc(uniform_ptr((const char*)base + row0 * row_bytes), (short)0,
                                                __builtin_amdgcn_readfirstlane(rows * row_bytes), kBufferConfig)) {}
   __device__ __forceinline__ u32x4 load16(uint32_t lane, int scalar) const {
-    return __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane, scalar, 0);
+    return __builtin_amdgcn_raw_buffer_load_b128(rsrc, lane + scalar, 0, 0);
   }
   __device__ __forceinline__ float load4(uint32_t lane, int scalar) const {
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane, scalar, 0));
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, lane + scalar, 0, 0));
   }
-  // (The offsets are added here and not left to the instruction: behind a
-  // 16-byte store without a scalar offset the compiler keeps its data registers
-  // for one more instruction.  With one it does not, and the next instruction's
-  // result was seen in the stored rows on gfx950.)
   __device__ __forceinline__ void store16(u32x4 v, uint32_t lane, int scalar) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, lane + scalar, 0, 0);
   }
   __device__ __forceinline__ void store4(float v, uint32_t lane, int scalar) const {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, lane, scalar, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, lane + scalar, 0, 0);
   }
 };
 
