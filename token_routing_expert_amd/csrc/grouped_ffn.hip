@@ -2043,7 +2043,13 @@ bool small_tiles(int64_t max_rows, int E) { return max_rows <= 64 * (int64_t)E &
 // the 128-expert layer: down 881 -> 743 us, gate/up 1470 -> 1259 us).  With
 // more rows per expert such tails are rare and the always-issued extra load
 // costs more than it saves (down 74 -> 86 us at 512 rows per expert).
-bool tall_tiles(int64_t max_rows, int E) { return max_rows <= 384 * (int64_t)E; }
+// A tile's rows are addressed with 31 bits (kOutOfRange lies past them): the 32
+// rows more have to fit, rows of K bf16 that are read and of 4 N bytes, [dg | du]
+// or float32, that are written.  (256 rows do: d and I are below 2^21.)
+bool tall_tiles(int64_t max_rows, int E, int64_t K, int64_t N) {
+  const int64_t row_bytes = 2 * K > 4 * N ? 2 * K : 4 * N;
+  return max_rows <= 384 * (int64_t)E && (kTallRows + kTallExtra) * row_bytes <= (int64_t)kOutOfRange;
+}
 
 template <int EPI, bool BT>
 hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows, int E, int K, int N, int ldw,
@@ -2055,17 +2061,17 @@ hipError_t launch_auto(const bf16_t* a, const int32_t* offsets, int64_t max_rows
   constexpr bool kPart = kRowPart || (EPI == kEpiPlain && !BT);
   float* part = kPart ? tail_ws : nullptr;
   if constexpr (EPI == kEpiPlain && !BT) {
-    if (allow_tall && big_tiles(max_rows, E, K) && tall_tiles(max_rows, E) && row_token == nullptr)
+    if (allow_tall && big_tiles(max_rows, E, K) && tall_tiles(max_rows, E, K, N) && row_token == nullptr)
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, nullptr,
                                                              0, out2, aux, 1, tail_ws, sched, nullptr, wtiled);
   }
   if constexpr (EPI == kEpiSwiglu && !BT) {
-    if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E))
+    if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E, K, N))
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                              a_rows, out2, aux, 1, nullptr, sched, nullptr, wtiled);
   }
   if constexpr (kRowPart || (EPI == kEpiPlain && BT)) {
-    if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E))
+    if (big_tiles(max_rows, E, K) && tall_tiles(max_rows, E, K, N))
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, out, s, row_token,
                                                              a_rows, out2, aux, 1, part, sched, row_w, wtiled, kept);
   }
@@ -2225,7 +2231,7 @@ hipError_t launch_keep(const bf16_t* x, const int32_t* offsets, int64_t max_rows
 }  // namespace
 
 int64_t keep_extra_floats(int64_t max_rows, int E, int d, int I) {
-  if (!big_tiles(max_rows, E, d) || !tall_tiles(max_rows, E)) return 0;
+  if (!big_tiles(max_rows, E, d) || !tall_tiles(max_rows, E, d, I)) return 0;
   return (int64_t)E * kTallExtra * 2 * I;
 }
 
@@ -2265,7 +2271,7 @@ hipError_t launch_rows32(const bf16_t* a, const int32_t* offsets, int64_t max_ro
   constexpr int EPI = kEpiRows32;
   bf16_t* o = (bf16_t*)out;
   if (big_tiles(max_rows, E, K)) {
-    if (n_split == 1 && tall_tiles(max_rows, E))
+    if (n_split == 1 && tall_tiles(max_rows, E, K, N))
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows,
                                                              nullptr, nullptr, 1, tail_ws, sched);
     return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows, nullptr,
