@@ -10,7 +10,8 @@
 // a NaN scale.  The floor keeps 127 / amax finite; what lies below it rounds to
 // the code 0.  A quotient is formed with the hardware's reciprocal (one step
 // off): a code differs from the exact quotient's only where that lies within
-// 2^-15 of a half, by one.
+// 2^-15 of a half, by one.  That reciprocal has no subnormal results, so it is
+// taken of 2^-8 amax: from 2^126 on it would be zero otherwise.
 #pragma once
 
 #include "common.hpp"
@@ -26,7 +27,7 @@ __device__ __forceinline__ void keep_scale(uint32_t amax_bits, float& scale, flo
   const float amax = __builtin_bit_cast(float, amax_bits > kFloor ? amax_bits : kFloor);
   const bool finite = amax_bits < 0x7F800000u;
   scale = finite ? amax * (1.f / kTop) : __builtin_bit_cast(float, 0x7FC00000u);
-  inv = finite ? kTop * __builtin_amdgcn_rcpf(amax) : 0.f;
+  inv = finite ? kTop * 0x1p-8f * __builtin_amdgcn_rcpf(amax * 0x1p-8f) : 0.f;
 }
 
 // Four codes, the first in the lowest byte.  |v inv| <= 127 (1 + 2^-21), and
@@ -41,16 +42,13 @@ __device__ __forceinline__ uint32_t keep_codes4(float a, float b, float c, float
   return __builtin_amdgcn_perm(ib, ia, 0x0c0c0400u) | __builtin_amdgcn_perm(id, ic, 0x04000c0cu);
 }
 
-// The values of four codes.  With the sign bits flipped a byte is code + 128,
-// which converts in one instruction; (code + 128) s - 128 s is exact before its
-// one rounding.
+// The values of four codes (the conversion takes a byte with its sign; the product
+// is rounded once, and finite wherever the values that were kept are).
 __device__ __forceinline__ void keep_values4(uint32_t codes, float s, float* v) {
-  const uint32_t b = codes ^ 0x80808080u;
-  const float off = -128.f * s;
-  v[0] = fmaf((float)(b & 0xFFu), s, off);
-  v[1] = fmaf((float)((b >> 8) & 0xFFu), s, off);
-  v[2] = fmaf((float)((b >> 16) & 0xFFu), s, off);
-  v[3] = fmaf((float)(b >> 24), s, off);
+  v[0] = (float)(int8_t)codes * s;
+  v[1] = (float)(int8_t)(codes >> 8) * s;
+  v[2] = (float)(int8_t)(codes >> 16) * s;
+  v[3] = (float)(int8_t)(codes >> 24) * s;
 }
 
 // The same with two 16-bit codes a dword.
@@ -60,10 +58,8 @@ __device__ __forceinline__ uint32_t keep_codes2(float a, float b, float inv) {
                                __builtin_bit_cast(uint32_t, fmaf(a, inv, kRound)), 0x05040100u);
 }
 __device__ __forceinline__ void keep_values2(uint32_t codes, float s, float* v) {
-  const uint32_t b = codes ^ 0x80008000u;
-  const float off = -32768.f * s;
-  v[0] = fmaf((float)(b & 0xFFFFu), s, off);
-  v[1] = fmaf((float)(b >> 16), s, off);
+  v[0] = (float)(int16_t)codes * s;
+  v[1] = (float)(int16_t)(codes >> 16) * s;
 }
 
 // max over 16 consecutive lanes (quads, then mirrored halves)
