@@ -1917,7 +1917,9 @@ constexpr int64_t kSplitMaxRows = 256;
 constexpr int kSplitMax = 8;
 constexpr int kSplitMinStages = 16;
 
-// One thread per 4 columns of a row.
+// One thread per 4 columns of a row, counted through all rows (a grid with a line
+// for each row has more lines than the 65536 that HIP promises, and leaves 240 of
+// 256 threads idle in rows of 64 columns).
 // With row_token (one pair per token) the rounded row goes, times its
 // routing weight row_w[r] and rounded again, to its token's row of out
 // ([out_rows, N]) instead of row r.
@@ -1926,10 +1928,10 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
                                                    int N, bf16_t* __restrict__ out,
                                                    const int32_t* __restrict__ row_token,
                                                    const float* __restrict__ row_w, int64_t out_rows) {
-  const int64_t r = blockIdx.y;
-  const int c = 4 * (blockIdx.x * blockDim.x + threadIdx.x);
-  const int64_t n_rows = clampi<int64_t>(offsets[E], 0, max_rows);
-  if (r >= n_rows || c >= N) return;
+  const uint32_t vecs = (uint32_t)N / 4, i = blockIdx.x * blockDim.x + threadIdx.x;   // (below 2^30)
+  const int64_t r = i / vecs;
+  const int c = 4 * (int)(i % vecs);
+  if (r >= clampi<int64_t>(offsets[E], 0, max_rows)) return;
   f32x4 sum = *(const f32x4*)(part + r * N + c);
   for (int sp = 1; sp < n_split; ++sp) sum += *(const f32x4*)(part + ((int64_t)sp * max_rows + r) * N + c);
   const uint2 y = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
@@ -1946,6 +1948,8 @@ __global__ __launch_bounds__(256) void k_split_sum(const float* __restrict__ par
   for (int v = 0; v < 4; ++v) f[v] = fmaf(w, f[v], 0.f);
   *(uint2*)(out + t * N + c) = pack4(f);
 }
+
+unsigned split_sum_blocks(int64_t max_rows, int N) { return (unsigned)ceil_div(max_rows * (N / 4), 256); }
 
 // The split tail's sums: block (x, y) takes rows 4 y .. 4 y + 3 of split
 // tile x, one thread per 4 columns; it adds the tile's pieces in piece order
@@ -2149,9 +2153,9 @@ hipError_t launch_down_bf16(const bf16_t* h, const int32_t* expert_offsets, int6
                 : launch_dma<kEpiPartial>(h, expert_offsets, max_rows, E, I, d, d, w_down, nullptr, s, nullptr, 0,
                                           nullptr, nullptr, n_split, split_ws, nullptr, nullptr, wtiled);
       if (e != hipSuccess) return e;
-      const dim3 grid((unsigned)ceil_div(d / 4, 256), (unsigned)max_rows);
-      k_split_sum<<<grid, 256, 0, s>>>(split_ws, n_split, expert_offsets, E, max_rows, d, sc ? sc->out : y_perm,
-                                       sc ? sc->row_token : nullptr, sc ? sc->row_w : nullptr, sc ? sc->T : 0);
+      k_split_sum<<<split_sum_blocks(max_rows, d), 256, 0, s>>>(
+          split_ws, n_split, expert_offsets, E, max_rows, d, sc ? sc->out : y_perm, sc ? sc->row_token : nullptr,
+          sc ? sc->row_w : nullptr, sc ? sc->T : 0);
       return hipGetLastError();
     }
   }
@@ -2350,8 +2354,8 @@ hipError_t launch_down_rows32(const bf16_t* h, const int32_t* expert_offsets, in
 
 hipError_t launch_split_sum(const float* part, int n_split, const int32_t* expert_offsets, int E, int64_t max_rows,
                             int N, bf16_t* out, hipStream_t s) {
-  k_split_sum<<<dim3((unsigned)ceil_div(N / 4, 256), (unsigned)max_rows), 256, 0, s>>>(
-      part, n_split, expert_offsets, E, max_rows, N, out, nullptr, nullptr, 0);
+  k_split_sum<<<split_sum_blocks(max_rows, N), 256, 0, s>>>(part, n_split, expert_offsets, E, max_rows, N, out, nullptr,
+                                                            nullptr, 0);
   return hipGetLastError();
 }
 
