@@ -117,3 +117,35 @@ def test_the_largest_float32_is_kept(tre, rows):
                                         base.put(np.zeros((1, n, d)), "f32"))
     base.sync()
     ref.check_codes(q.cpu().numpy(), s.cpu().numpy(), np.repeat(wgu[0, :1], rows, 0), np.zeros((rows, 2 * n)))
+
+
+@pytest.mark.parametrize("T_,E,n", [(1400, 64, 192), (800, 8, 832), (2048, 8, 832), (4096, 4, 832)],
+                         ids=["64-row tiles", "128-row tiles", "tall tiles", "256-row tiles"])
+def test_an_infinite_h_is_infinite_in_its_weight_gradient(tre, T_, E, n):
+    """One kept row whose silu(g) u passes float32 in one column: its routing weight's gradient is <dh, h> = infinity (dh
+    is positive there), and every other row's is exact.  n is no multiple of a tile's 256 columns, and the column lies
+    in the first block of the tile that ends inside."""
+    d, k = 128, 1
+    at = (n - 1) // 256 * 256
+    idx, w = base.route_given(T_, E, k, T_, drop=0)
+    x, dout, wgu, wd, _ = base.exact_inputs(T_, E, d, n, T_)
+    u = base.sparse_ints((T_, n), 0.7, T_, 2)
+    bad = 77                                # the pair; its grouped row:
+    offs, tok, row = base.grouping(tre, base.put(x, "bf16"), idx, E)
+    r = int(row[bad])
+    u[r, at:at + 64] = 0.0
+    u[r, at + 5] = 1.0
+    dout[bad], wd[idx[bad, 0], at + 5] = np.abs(dout[bad]), 1.0
+    dout[bad, 0] = 1.0
+    q, s = base.exact_checkpoint(u)
+    s[r, :, at // 64] = 1e20
+    got = tre.moe_backward_q8(base.put(x, "bf16"), base.put(wgu, "bf16"), base.put(wd, "bf16"), k,
+                              base.put(dout, "bf16"), to_device(idx), to_device(w), tre.Checkpoint(offs, tok, row, q, s))
+    base.sync()
+    dw = base.host(got["dtopk_w"]).reshape(-1)
+    want = np.zeros(T_)
+    for e, pairs in enumerate(base.group_numpy(idx, E)):
+        rows = row[to_device(pairs)].cpu().numpy()
+        want[pairs] = (64 * u[rows] * (dout[pairs] @ wd[e].T)).sum(1)
+    assert dw[bad] == np.inf
+    assert np.array_equal(np.delete(dw, bad), np.delete(want, bad))

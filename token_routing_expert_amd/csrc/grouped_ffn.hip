@@ -1024,7 +1024,7 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
               const float sg = __builtin_amdgcn_rcpf(1.f + __expf(-g[v]));
               const float silu = g[v] * sg;
               h[v] = silu * u4[v];
-              part = fmaf(h[v], there ? dh : 0.f, part);
+              part = fmaf(h[v], dh, part);
               const float wdh = w * dh;
               dg[v] = wdh * u4[v] * (sg + silu * (1.f - sg));
               du[v] = wdh * silu;
@@ -1045,6 +1045,8 @@ __global__ __launch_bounds__(128 * WM, (OCC * WM + 1) / 2) void k_grouped_gemm(
             h_rows.store16(vh, h_lane, (r0 * N + c + 16 * p) * 2);
           }
         }
+        // (of no column: whatever the tile's first ones gave, which may be infinite)
+        part = there ? part : 0.f;
         // (the row's other 4-column groups are in lane l + 32)
         const uint32_t bits = __builtin_bit_cast(uint32_t, part);
         const auto sw = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
