@@ -57,7 +57,7 @@ extern "C" {
  * (MOE_BF16: held meanwhile as whole multiples of a scale as above, of 16 bits,
  * off by at most amax / 65534).  MOE_BF16: float32 accumulation; h, dg and du
  * are rounded to bf16 before the products that read them (in calls of few rows
- * and narrow experts they stay float32, by a rule on the sizes), and every
+ * whose sums are not long they stay float32, by a rule on the sizes), and every
  * gradient once; MOE_F32: float32 throughout.  The order of every sum
  * depends on the sizes only, so equal calls give equal bits.
  *   x_perm, dy_perm [max_rows, d] dt; expert_offsets [E+1]

@@ -10,3 +10,16 @@ def test_the_widest_rows_take_no_tall_tiles():
     size = tre.load().moe_grouped_ffn_train_workspace_size
     tall, widest = size(288, 1, 128, 1864064, 1), size(288, 1, 128, WIDEST, 1)
     assert tall > (576 + 256) * 1864064 and 576 * WIDEST < widest < tall
+
+
+def test_the_least_calls_go_to_the_kernels_of_few_tiles_unless_a_sum_is_long():
+    """Those kernels' forward of d <= 768 has h in float32 for its workspace, and nothing else.  A workgroup there walks d
+    or 2 I terms by itself, which long sums are too slow for, unless experts without rows cost more elsewhere."""
+    size = tre.load().moe_grouped_ffn_train_workspace_size
+
+    def few(rows, E, d, I):
+        return size(rows, E, d, I, 1) == -(-4 * rows * I // 256) * 256
+
+    assert few(1, 1, 64, 64) and few(64, 1, 64, 2880) and few(16, 8, 512, 512) and few(8, 8, 64, 1024)
+    assert not few(64, 1, 64, 8192) and not few(1, 1, 512, 16384) and not few(128, 8, 64, 65536)
+    assert few(1, 64, 512, 8192)

@@ -402,16 +402,23 @@ unsigned row_tiles(int64_t max_rows, int E) { return (unsigned)(max_rows / kRows
 // 512 x 512: 75 and 103; 264, 2, 640 x 704: 74 and 109; 10, 60, 512 x 512: 63 and
 // 106; 30, 100, 256 x 384: 52 and 129; above, 512, 16, 512 x 512: 88 and 82; 100,
 // 1, 1024 x 1024: 88 and 77; 1500, 3, 128 x 1024: 116 and 99.
-// The least bf16 calls come here at any width (8, 128, 1024 x 1024: 302 and 383; 37,
-// 11, 832 x 64: 45 and 64; the dearest, 4, 1, 64 x 2880: 86 and 59): rounding h, dg
+// The least bf16 calls come here too where that costs little: rounding h, dg
 // and du to bf16 makes the outputs' error 1.4 times their own rounding's where many
 // roundings average out, but up to 1.55 times by chance over a few hundred values.
+// A workgroup walks the longest sum, d or 2 I terms, by itself (9 ns a term), where
+// the other kernels cut it into ranges; they in turn write the zero gradients of
+// experts without rows at half the rate.  Rows, experts, d x I, this way and the
+// other: 8, 128, 1024 x 1024: 291 and 680; 37, 11, 832 x 64: 41 and 63; 64, 1, 2880
+// x 64: 61 and 54; the dearest, 64, 1, 64 x 2880: 98 and 63; 1, 8, 8192 x 8192: 1353
+// and 2563; above, 16, 1, 8192 x 128: 114 and 78; 16, 1, 128 x 8192: 209 and 89; 1, 1,
+// 512 x 65536: 2300 and 451.
 bool small_products(int64_t max_rows, int E, int d, int I, bool bf16) {
   const int64_t tiles = max_rows / 64 + std::min<int64_t>(E, max_rows);
   const int width = std::min(d, I);
   const int64_t t = tiles * ceil_div(width, 128);
   if (bf16)   // (2^32: the weight gradients' tiles have to fit a grid of 2^32 threads)
-    return (max_rows * width <= 8192 && (int64_t)E * d * I <= ((int64_t)1 << 32)) ||
+    return (max_rows * width <= 8192 && (int64_t)E * d * I <= ((int64_t)1 << 32) &&
+            std::max<int64_t>(d, 2 * (int64_t)I) <= 6000 + std::max<int64_t>(E - max_rows, 0) * d * I / 3000) ||
            (max_rows <= 400 * (int64_t)E && t <= 64 && std::max(d, I) <= 768);
   return ((max_rows <= 128 * (int64_t)E && t <= 160) || (max_rows <= 1024 * (int64_t)E && t <= 80)) &&
          (int64_t)E * d * I <= ((int64_t)1 << 24);
