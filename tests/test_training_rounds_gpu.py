@@ -42,7 +42,7 @@ def rounds(kind, counts, columns):
 
 def right_kind(kind, counts):
     R, E = sum(counts) + exact.EXTRA, len(counts)
-    return {"256": R > 384 * E, "tall": 128 * E <= R <= 384 * E, "128": 64 * E < R < 128 * E,
+    return {"256": R > 384 * E, "tall": 128 * E <= R <= 288 * E, "128": 64 * E < R < 128 * E,
             "64": R <= 64 * E and E <= 128}[kind]
 
 

@@ -2049,12 +2049,23 @@ bool small_tiles(int64_t max_rows, int E) { return max_rows <= 64 * (int64_t)E &
 // the 128-expert layer: down 881 -> 743 us, gate/up 1470 -> 1259 us).  With
 // more rows per expert such tails are rare and the always-issued extra load
 // costs more than it saves (down 74 -> 86 us at 512 rows per expert).
+// `mean`, that limit, is 288 for the training forward (gate/up with its checkpoint,
+// float32 rows of y), whose epilogue has a tall tile's rows in a pass of their own;
+// the products of the backward, with weights as rows of k, have 384.  Measured on
+// 256-row tiles and on tall ones throughout, us, forward and backward (with a
+// checkpoint), rows around the mean by chance: 128 experts, 2880 x
+// 2880, mean 256: 2180 and 1895, 5359 and 4875; 280: 2731 and 2248, 6246 and 5242; 296:
+// 2725 and 2738, 6456 and 5951; 320: 2891 and 3045, 6566 and 6407; 384: 3003 and 3224,
+// 6827 and 6753; 450: 3092 and 3368, 7073 and 7146.  32 experts, 280: 670 and 567, 1444
+// and 1295; 320: 691 and 772, 1542 and 1525; 450: 751 and 834, 1761 and 1771.  16 experts,
+// 1024 x 2816, 280: 154 and 143, 303 and 286; 320: 159 and 172, 320 and 333.
 // A tile's rows are addressed with 31 bits (kOutOfRange lies past them): the 32
 // rows more have to fit, rows of K bf16 that are read and of 4 N bytes, [dg | du]
 // or float32, that are written.  (256 rows do: d and I are below 2^21.)
-bool tall_tiles(int64_t max_rows, int E, int64_t K, int64_t N) {
+constexpr int kTallMean = 384, kTallMeanForward = kTallRows + kTallExtra;
+bool tall_tiles(int64_t max_rows, int E, int64_t K, int64_t N, int mean = kTallMean) {
   const int64_t row_bytes = 2 * K > 4 * N ? 2 * K : 4 * N;
-  return max_rows <= 384 * (int64_t)E && (kTallRows + kTallExtra) * row_bytes <= (int64_t)kOutOfRange;
+  return max_rows <= mean * (int64_t)E && (kTallRows + kTallExtra) * row_bytes <= (int64_t)kOutOfRange;
 }
 
 template <int EPI, bool BT>
@@ -2237,7 +2248,7 @@ hipError_t launch_keep(const bf16_t* x, const int32_t* offsets, int64_t max_rows
 }  // namespace
 
 int64_t keep_extra_floats(int64_t max_rows, int E, int d, int I) {
-  if (!big_tiles(max_rows, E, d) || !tall_tiles(max_rows, E, d, I)) return 0;
+  if (!big_tiles(max_rows, E, d) || !tall_tiles(max_rows, E, d, I, kTallMeanForward)) return 0;
   return (int64_t)E * kTallExtra * 2 * I;
 }
 
@@ -2277,7 +2288,7 @@ hipError_t launch_rows32(const bf16_t* a, const int32_t* offsets, int64_t max_ro
   constexpr int EPI = kEpiRows32;
   bf16_t* o = (bf16_t*)out;
   if (big_tiles(max_rows, E, K)) {
-    if (n_split == 1 && tall_tiles(max_rows, E, K, N))
+    if (n_split == 1 && tall_tiles(max_rows, E, K, N, BT ? kTallMean : kTallMeanForward))
       return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows,
                                                              nullptr, nullptr, 1, tail_ws, sched);
     return launch_dma<EPI, BT, 32, 1, 4, 4, 4, true>(a, offsets, max_rows, E, K, N, ldw, w, o, s, row_token, a_rows, nullptr,
