@@ -11,7 +11,7 @@ from helpers import to_device
 
 OFF = 1.01 * 64 / 65534      # 16-bit codes of magnitudes up to 64: u is off by that at most
 HALF, SUM = 2.0 ** -8, 2.0 ** -23
-EXTRA = 2                    # rows behind the last expert
+EXTRA = 2                    # rows behind the last expert, where a check is not told
 
 
 def gen(seed):
@@ -116,14 +116,15 @@ def forward_rows(xs, wgu, wd, I, q, s):
     return want
 
 
-def check_forward(tre, counts, d, I, dtype=t.bfloat16):
+def check_forward(tre, counts, d, I, dtype=t.bfloat16, extra=EXTRA):
     E, R = len(counts), sum(counts)
     g = gen(d + I + R)
     wgu, wd = weights(E, d, I, g, dtype)
-    x, _ = rows_of(R + EXTRA, d, g, dtype)
-    y = sentinel((R + EXTRA, d), dtype)
-    q = t.full((R + EXTRA, 2 * I), 77, dtype=t.int8, device="cuda")
-    s = t.full((R + EXTRA, 2, I // 64), -3.0, device="cuda")
+    x, _ = rows_of(R + extra, d, g, dtype)
+    x[R:] = float("nan")
+    y = sentinel((R + extra, d), dtype)
+    q = t.full((R + extra, 2 * I), 77, dtype=t.int8, device="cuda")
+    s = t.full((R + extra, 2, I // 64), -3.0, device="cuda")
     tre.moe_grouped_ffn_train(x, offsets(counts), wgu, wd, y_perm=y, gu_q=q, gu_s=s)
     t.cuda.synchronize()
     untouched(y[R:])
@@ -164,19 +165,20 @@ def backward_rows(xs, dys, wgu, wd, I, v_of, dwgu, dwd, w, again, name):
     return want_x, err_x, dot
 
 
-def check_backward(tre, counts, d, I, again, dtype=t.bfloat16):
+def check_backward(tre, counts, d, I, again, dtype=t.bfloat16, extra=EXTRA):
     """again (bf16): g | u computed from x and held in 16-bit codes: g stays 64 but for float32's last places, and u is
     off by OFF at most, so du is exact, and dg = dh u and h = 64 u are off by |dh| OFF, 64 OFF and their rounding."""
     E, R = len(counts), sum(counts)
     g = gen(d + I + R)
     wgu, wd = weights(E, d, I, g, dtype)
-    x, dy = rows_of(R + EXTRA, d, g, dtype)
+    x, dy = rows_of(R + extra, d, g, dtype)
+    x[R:], dy[R:] = float("nan"), float("inf")
     u, kw = None, {}
     if not again:
-        u, q, s = checkpoint(R + EXTRA, I, 7)
+        u, q, s = checkpoint(R + extra, I, 7)
         s[R:] = float("nan")
         kw = dict(gu_q=q, gu_s=s)
-    dx, dwgu, dwd = sentinel((R + EXTRA, d), dtype), sentinel((E, d, 2 * I), dtype), sentinel((E, I, d), dtype)
+    dx, dwgu, dwd = sentinel((R + extra, d), dtype), sentinel((E, d, 2 * I), dtype), sentinel((E, I, d), dtype)
     tre.moe_grouped_ffn_backward(x, offsets(counts), wgu, wd, dy, dx_perm=dx, dw_gate_up=dwgu, dw_down=dwd, **kw)
     t.cuda.synchronize()
     untouched(dx[R:])
