@@ -53,3 +53,31 @@ def test_layers(tre, T_, k, E, drop, d, I, dtype):
 def test_float32_steps_of_some_thousand_rows(tre, counts, d, I):
     exact.check_forward(tre, counts, d, I, torch.float32)
     exact.check_backward(tre, counts, d, I, False, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T_,k,E,d,I", [(40, 3, 5, 64, 128), (700, 2, 16, 128, 832), (2000, 2, 4, 128, 832)])
+def test_dropped_pairs_hide_what_is_theirs(tre, T_, k, E, d, I, dtype):
+    """Weights of dropped pairs, and rows of tokens that have no other pair, may hold anything: outputs are those of zeros
+    there, bit for bit."""
+    idx = pairs(T_, k, E, 0.4, T_)
+    idx[::7] = -1
+    idx[1::7, 0] = E + 3                    # an id that is no expert's here drops its pair too
+    gone = torch.from_numpy((idx < 0) | (idx >= E)).cuda()
+    g = exact.gen(T_)
+    wgu, wd = exact.weights(E, d, I, g, TYPES[dtype])
+    x, dout = exact.rows_of(T_, d, g, TYPES[dtype])
+    w = torch.rand((T_, k), generator=g, device="cuda")
+    idx = torch.from_numpy(idx).cuda()
+    got = []
+    for hidden in (0.0, float("nan"), float("inf"), -3e38):
+        xs, ds, ws = x.clone(), dout.clone(), w.clone()
+        ws[gone] = hidden
+        xs[gone.all(1)], ds[gone.all(1)] = hidden, hidden
+        out, _, _, kept = tre.moe_forward_train_q8(xs, wgu, wd, k, topk_idx=idx, topk_w=ws)
+        r = tre.moe_backward_q8(xs, wgu, wd, k, ds, idx, ws, kept, want_dlogits=True)
+        got.append([out, *r.values()])
+    torch.cuda.synchronize()
+    for other in got[1:]:
+        for a, b, name in zip(got[0], other, ("out", "dx", "dw_gate_up", "dw_down", "dtopk_w", "dlogits")):
+            assert torch.equal(a, b), name

@@ -284,10 +284,10 @@ __global__ __launch_bounds__(kThreads) void k_combine_grad(
       for (int64_t n = lane; n < n_parts; n += kWave) sum += dot[r * n_parts + n];
 #pragma unroll
       for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+      inner = fmaf(pair_w[t * k + j], sum, inner);   // (a dropped pair's weight may be anything)
     }
     if (lane == 0) dw[t * k + j] = sum;
     if (dlogits) my_dw[j] = sum;
-    inner = fmaf(pair_w[t * k + j], sum, inner);
   }
   if (!dlogits) return;
   for (int e = lane; e < E; e += kWave) {
