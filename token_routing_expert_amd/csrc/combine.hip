@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_bwd(
       for (int off = kWave / 2; off > 0; off >>= 1) dot += __shfl_xor(dot, off, kWave);
     }
     if (lane == 0) dw[t * k + j] = dot;
-    my_dw[j] = dot;
+    if (dlogits) my_dw[j] = dot;   // (k <= E then; given pairs may be more than my_dw holds)
     inner = fmaf(w, dot, inner);
   }
   if (!dlogits) return;
