@@ -9,7 +9,8 @@
  *
  * Rows, weights, gradients, codes and workspaces begin at multiples of 16
  * bytes (MOE_ERR_ARG otherwise); scales, indices and routing weights at
- * multiples of their own 4.  Limits beside moe.h's: d and I below 2^21, grouped
+ * multiples of their own 4.  No output overlaps an input, another output or the
+ * workspace.  Limits beside moe.h's: d and I below 2^21, grouped
  * rows * max(d, 2I) below 2^31, E * 2*d*I below 2^34, a layer's T*d below 2^30.
  *
  * A workspace size holds for its arguments alone: fewer rows can need a larger
@@ -27,8 +28,9 @@
  * 4d + 6I.  A value is off by at most s / 2 = amax / 254: 0.57% of the
  * standard deviation for normally distributed values (e4m3 codes: 2.6%).  A
  * block that holds an infinity or a NaN gets a NaN scale, and its values are
- * NaN.  Gradients from a checkpoint are those of the formulas below at the
- * kept values of g and u; the forward's own output does not pass through them.
+ * NaN; every finite block is kept, up to the largest float32.  Gradients from a
+ * checkpoint are those of the formulas below at the kept values of g and u; the
+ * forward's own output does not pass through them.
  */
 #ifndef TRE_MOE_TRAINING_H
 #define TRE_MOE_TRAINING_H
@@ -55,10 +57,11 @@ extern "C" {
  *   dW_down[e] = sum_r h^T dy           (zero for an expert without rows)
  * gu_q and gu_s: a checkpoint, or both NULL: g | u are computed again from x
  * (MOE_BF16: held meanwhile as whole multiples of a scale as above, of 16 bits,
- * off by at most amax / 65534).  MOE_BF16: float32 accumulation; h, dg and du
- * are rounded to bf16 before the products that read them (in calls of few rows
- * whose sums are not long they stay float32, by a rule on the sizes), and every
- * gradient once; MOE_F32: float32 throughout.  The order of every sum
+ * off by at most amax / 65534: closer than bf16 for values down to 1 / 128 of
+ * their block's largest, coarser below).  MOE_BF16: float32 accumulation; h, dg
+ * and du are rounded to bf16 before the products that read them (in calls of few
+ * rows whose sums are not long they stay float32, by a rule on the sizes), and
+ * every gradient once; MOE_F32: float32 throughout.  The order of every sum
  * depends on the sizes only, so equal calls give equal bits.
  *   x_perm, dy_perm [max_rows, d] dt; expert_offsets [E+1]
  *   y_perm, dx_perm [max_rows, d] dt (outputs; rows >= expert_offsets[E], of
@@ -98,7 +101,8 @@ moe_status moe_grouped_ffn_backward(const void* x_perm, const int32_t* expert_of
  *   moe_route_topk, zero for experts not selected (NULL to skip)
  *   x, dout [T, d] dt; topk_idx, topk_w [T, k] and the five kept arrays: as
  *     the forward filled or read them (rows of a checkpoint beyond
- *     expert_offsets[E] are not read)
+ *     expert_offsets[E] are not read; row_token has to be given, and is not
+ *     read either: pair_row says where a token's rows are)
  *   dx [T, d], dw_gate_up [E, d, 2I], dw_down [E, I, d] dt, dtopk_w [T, k]
  *     float32 (outputs, overwritten; dtopk_w is 0 for dropped pairs)
  *   workspace >= the matching *_workspace_size(); T == 0 zeroes the weight
