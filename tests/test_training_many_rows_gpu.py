@@ -19,3 +19,12 @@ def test_forward(tre, counts, d, I):
 @pytest.mark.parametrize("counts,d,I", [([70000], 128, 4096), ([66000], 256, 8000), ([65000, 0, 5100], 64, 4096)])
 def test_backward(tre, counts, d, I):
     exact.check_backward(tre, counts, d, I, again=False)
+
+
+# the most rows that d x I allows, and an expert that has nearly all of them
+@pytest.mark.parametrize("counts,d,I", [([9_000_000, 7_777_000], 64, 64), ([100, 5_592_000, 0], 128, 192)])
+def test_the_most_rows(tre, counts, d, I):
+    assert sum(counts) * 2 * I < 1 << 31 < (sum(counts) + 2000) * 2 * I
+    exact.check_forward(tre, counts, d, I)
+    exact.check_backward(tre, counts, d, I, again=False)
+    exact.check_backward(tre, counts, d, I, again=True)

@@ -2,6 +2,7 @@
 rows would pass 31-bit byte offsets: bit for bit where every sum is exact."""
 import numpy as np
 import pytest
+import torch
 
 import training_exact as exact
 from test_training_gpu import tre  # noqa: F401  (the fixture)
@@ -33,3 +34,9 @@ def test_few_rows_and_long_sums(tre, counts, d, I):
     exact.check_forward(tre, counts, d, I)
     exact.check_backward(tre, counts, d, I, again=False)
     exact.check_layer(tre, np.repeat(np.arange(len(counts)), counts)[:, None].astype(np.int32), d, len(counts), I)
+
+
+@pytest.mark.parametrize("d,I", [(128, WIDEST), (WIDEST, 128)])
+def test_float32(tre, d, I):
+    exact.check_forward(tre, ROWS, d, I, torch.float32)
+    exact.check_backward(tre, ROWS, d, I, False, torch.float32)
